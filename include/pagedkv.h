@@ -336,6 +336,215 @@ PAGEDKV_API int paged_decode_attn_fp8k_static_scratch(
     float k_scale, uint32_t q_stride, uint32_t sliding_window, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Sliding window with sinks (the source pages have the window only; dropping
+ * a sequence's first tokens costs a model that rests attention on them far
+ * more than any others). As the calls without `_sinks`, but a query at position
+ * P attends every position p <= P with
+ *   sliding_window == 0  or  p > P - sliding_window  or  p < num_sinks.
+ * num_sinks 0 is the plain window; with sliding_window 0 it changes nothing.
+ * Blocks that hold no attended position are not read: their table entries may
+ * hold anything (kv_free_window_blocks makes them -1).
+ * ---------------------------------------------------------------------- */
+PAGEDKV_API int paged_decode_attn_bf16_sinks(const kv_bf16_t *q, const kv_bf16_t *k_cache,
+                                             const kv_bf16_t *v_cache, float *output, const int32_t *block_tables,
+                                             const int32_t *seq_lens, uint32_t max_blocks_per_seq,
+                                             uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads,
+                                             uint32_t head_dim, uint32_t block_size, float inv_sqrt_d,
+                                             uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks,
+                                             void *stream);
+
+PAGEDKV_API int paged_decode_attn_fp8k_sinks(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
+                                             const kv_bf16_t *v_cache, float *output, const int32_t *block_tables,
+                                             const int32_t *seq_lens, uint32_t max_blocks_per_seq,
+                                             uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads,
+                                             uint32_t head_dim, uint32_t block_size, float inv_sqrt_d,
+                                             float k_scale, uint32_t q_stride, uint32_t sliding_window,
+                                             uint32_t num_sinks, void *stream);
+
+PAGEDKV_API int paged_decode_attn_fp8_sinks(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
+                                            const kv_e4m3_t *v_cache_fp8, float *output,
+                                            const int32_t *block_tables, const int32_t *seq_lens,
+                                            uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_heads,
+                                            uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size,
+                                            float inv_sqrt_d, float k_scale, float v_scale, uint32_t q_stride,
+                                            uint32_t sliding_window, uint32_t num_sinks, void *stream);
+
+/* Multi-token forms: as paged_prefill_attn_* with the mask above, inv_sqrt_d >
+ * 0, and the output rows in BF16, bf16[num_q_tokens, num_q_heads, head_dim],
+ * 16-byte aligned: the softmax weights enter the products rounded to 11 bits,
+ * so a 32-bit row would hold nothing that BF16's 8 bits drop but rounding, at
+ * twice the bytes. A V value that is not finite makes the rows of every query
+ * whose keys share a 128-key tile with it non-finite. */
+PAGEDKV_API int paged_prefill_attn_bf16_sinks(const kv_bf16_t *q, const kv_bf16_t *k_cache,
+                                              const kv_bf16_t *v_cache, kv_bf16_t *output,
+                                              const int32_t *block_tables, const int32_t *seq_lens,
+                                              const int32_t *query_start_loc, uint32_t max_blocks_per_seq,
+                                              uint32_t num_seqs, uint32_t num_q_tokens, uint32_t num_q_heads,
+                                              uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size,
+                                              float inv_sqrt_d, uint32_t q_stride, uint32_t sliding_window,
+                                              uint32_t num_sinks, void *stream);
+
+PAGEDKV_API int paged_prefill_attn_fp8k_sinks(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
+                                              const kv_bf16_t *v_cache, kv_bf16_t *output,
+                                              const int32_t *block_tables, const int32_t *seq_lens,
+                                              const int32_t *query_start_loc, uint32_t max_blocks_per_seq,
+                                              uint32_t num_seqs, uint32_t num_q_tokens, uint32_t num_q_heads,
+                                              uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size,
+                                              float inv_sqrt_d, float k_scale, uint32_t q_stride,
+                                              uint32_t sliding_window, uint32_t num_sinks, void *stream);
+
+PAGEDKV_API int paged_prefill_attn_fp8_sinks(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
+                                             const kv_e4m3_t *v_cache_fp8, kv_bf16_t *output,
+                                             const int32_t *block_tables, const int32_t *seq_lens,
+                                             const int32_t *query_start_loc, uint32_t max_blocks_per_seq,
+                                             uint32_t num_seqs, uint32_t num_q_tokens, uint32_t num_q_heads,
+                                             uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size,
+                                             float inv_sqrt_d, float k_scale, float v_scale, uint32_t q_stride,
+                                             uint32_t sliding_window, uint32_t num_sinks, void *stream);
+
+/* ------------------------------------------------------------------------
+ * FP8 cache with one scale for each block and KV head (not on the pages, whose
+ * FP8 caches have one scale for a whole tensor: one outlier then sets the grid of
+ * every token). The codes are in uint8 pools of the usual layout, the scales in
+ * k_scales and v_scales, float32[num_blocks, num_kv_heads]; an element is its
+ * E4M3 code times the scale of its block and head.
+ *
+ * kv_write_fp8_block writes the tokens that a prefill with the same
+ * query_start_loc attends from: sequence s's last n_s = query_start_loc[s+1] -
+ * query_start_loc[s] positions (a decode step: query_start_loc = 0, 1, 2, ...).
+ * Query j of s is row query_start_loc[s] + j of key and value, at position
+ * seq_lens[s] - n_s + j, in block block_tables[s][position / block_size]. For
+ * each block that this touches, each head, and K and V each:
+ *   s' = the least power of two with |x| <= 448 s' for the finite new values x
+ *        of the block and head, at least 2^-60, and at least the block's
+ *        present scale where the block holds earlier positions of s
+ *   code = E4M3(x / s'), round to nearest even; NaN gives 0x7F, an infinity
+ *        +-448
+ *   where s' exceeds the present scale, the earlier positions' codes c become
+ *        E4M3(c * scale / s'): exact unless that is below 2^-6
+ * A block that holds no earlier position takes its scale from the new values
+ * alone, whatever its entry held. Rows of the block past seq_lens[s] stay as
+ * they are. A block may not be written for two sequences in one call (copy a
+ * shared one first: kv_fork_blocks, kv_copy_blocks). A negative table entry
+ * skips its positions, and positions below 0 or past the table are skipped. A
+ * bad query_start_loc sets bit 2 of the fault word, a sequence longer than its
+ * table bit 1; with bit 2 set, other sequences of the call may be skipped too.
+ *   key, value   device bf16 rows at element strides key_stride, value_stride
+ *                >= num_kv_heads * head_dim.
+ * Supported: head_dim 64, 128 or 256; block_size a power of two in [16, 256];
+ * code pools 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+PAGEDKV_API int kv_write_fp8_block(const kv_bf16_t *key, const kv_bf16_t *value, kv_e4m3_t *k_cache_fp8,
+                                   kv_e4m3_t *v_cache_fp8, float *k_scales, float *v_scales,
+                                   const int32_t *block_tables, const int32_t *seq_lens,
+                                   const int32_t *query_start_loc, uint32_t max_blocks_per_seq,
+                                   uint32_t num_seqs, uint32_t num_tokens, uint32_t num_kv_heads,
+                                   uint32_t head_dim, uint32_t block_size, uint32_t key_stride,
+                                   uint32_t value_stride, void *stream);
+
+/* Paged decode over that cache: as paged_decode_attn_fp8_sinks with each
+ * position's K and V scaled by its block's scales, any finite scales in [2^-60,
+ * 2^120]. head_dim 64, 128 or 256. */
+PAGEDKV_API int paged_decode_attn_fp8_block(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
+                                            const kv_e4m3_t *v_cache_fp8, const float *k_scales,
+                                            const float *v_scales, float *output, const int32_t *block_tables,
+                                            const int32_t *seq_lens, uint32_t max_blocks_per_seq,
+                                            uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads,
+                                            uint32_t head_dim, uint32_t block_size, float inv_sqrt_d,
+                                            uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks,
+                                            void *stream);
+
+/* Multi-token form over that cache: as paged_prefill_attn_fp8_sinks (BF16
+ * rows out), with the block scales. head_dim 64 or 128. */
+PAGEDKV_API int paged_prefill_attn_fp8_block(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
+                                             const kv_e4m3_t *v_cache_fp8, const float *k_scales,
+                                             const float *v_scales, kv_bf16_t *output, const int32_t *block_tables,
+                                             const int32_t *seq_lens, const int32_t *query_start_loc,
+                                             uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_tokens,
+                                             uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_dim,
+                                             uint32_t block_size, float inv_sqrt_d, uint32_t q_stride,
+                                             uint32_t sliding_window, uint32_t num_sinks, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of a cache (not on the pages): copying, sharing on a fork, freeing and
+ * compacting, all on device-resident block tables, with no host round trip.
+ * ref_counts int32[num_blocks] holds the number of table entries that name
+ * each block; a block whose count is 0 (or less) is free. Allocation takes the free blocks
+ * with the lowest ids, so every result is a function of the inputs alone. Ids
+ * and rows are checked against num_blocks and num_seqs on the device: one out of
+ * range is skipped and sets bit 4 of the fault word. The calls on one set of
+ * tables and counts belong on one stream, or in an order of the caller's.
+ *
+ * kv_copy_blocks: for every pool p and pair i, block dst_blocks[i] of pool p
+ * becomes a copy of block src_blocks[i]. A pair with a negative id is padding.
+ * No block may be the destination of two pairs, or of one and the source of
+ * another.
+ *   pools, block_bytes   HOST arrays of num_pools device base pointers and of
+ *                        the bytes of one block in each (e.g. every layer's K
+ *                        and V codes and their scales); read before the call
+ *                        returns.
+ *   src_blocks, dst_blocks   device int32[num_pairs].
+ * ---------------------------------------------------------------------- */
+PAGEDKV_API int kv_copy_blocks(void *const *pools, const size_t *block_bytes, uint32_t num_pools,
+                               const int32_t *src_blocks, const int32_t *dst_blocks, uint32_t num_pairs,
+                               uint32_t num_blocks, void *stream);
+
+/* Entries [first_block[s], end_block[s]) of each row s become -1 and their
+ * blocks' counts drop by one (rows with first >= end stay; the range is cut to
+ * the table). An entry whose block's count is 0 already sets bit 4.
+ *   block_tables int32[num_seqs, max_blocks_per_seq] and ref_counts, updated;
+ *   first_block, end_block  device int32[num_seqs]. */
+PAGEDKV_API int kv_free_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *first_block,
+                               const int32_t *end_block, uint32_t max_blocks_per_seq, uint32_t num_seqs,
+                               uint32_t num_blocks, void *stream);
+
+/* The same for the blocks that a window has left behind: those that hold
+ * neither a sink nor a position at or past seq_lens[s] - sliding_window, which
+ * no decode at this length or a later one, and no prefill of later tokens,
+ * attends. sliding_window 0 frees nothing. */
+PAGEDKV_API int kv_free_window_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *seq_lens,
+                                      uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks,
+                                      uint32_t block_size, uint32_t sliding_window, uint32_t num_sinks,
+                                      void *stream);
+
+/* Row dst_seqs[i] becomes a fork of row src_seqs[i], for every i < num_forks:
+ * the same length, the same full blocks (each counted once more; -1 entries
+ * stay -1), and for a partly filled last block a free block of its own, with
+ * the pair (copy_src[i], copy_dst[i]) to hand to kv_copy_blocks; (-1, -1)
+ * where there is none. The free blocks go to the forks in order of i. The
+ * destination rows must be free (released by kv_free_blocks): what they held
+ * is overwritten, not released. A row that two forks write, or that one
+ * writes and another reads, makes those forks invalid: an invalid fork
+ * (also: a row out of range, a length past the table) sets bit 4, one that
+ * finds no free block sets bit 5; either leaves its row as it was and gets the
+ * pair (-2, -2).
+ *   block_tables, seq_lens int32[num_seqs], ref_counts (16-byte aligned)
+ *   updated; src_seqs, dst_seqs device int32[num_forks]; copy_src, copy_dst
+ *   device int32[num_forks], written.
+ * Supported: num_seqs / 16 + num_forks up to 51,200 (shared memory of one CTA). */
+PAGEDKV_API int kv_fork_blocks(int32_t *block_tables, int32_t *seq_lens, int32_t *ref_counts,
+                               const int32_t *src_seqs, const int32_t *dst_seqs, int32_t *copy_src,
+                               int32_t *copy_dst, uint32_t num_forks, uint32_t max_blocks_per_seq,
+                               uint32_t num_seqs, uint32_t num_blocks, uint32_t block_size, void *stream);
+
+/* With U blocks in use, the i-th lowest used block with an id >= U moves to the
+ * i-th lowest free id below U, so that the blocks in use become 0 .. U-1. The
+ * call writes the new tables and counts and the list of moves; kv_copy_blocks
+ * moves the data (no source is a destination).
+ *   new_tables, new_ref_counts  the tables and counts after the moves; each may
+ *                be the input itself. An entry of block_tables that names a free
+ *                block becomes -1 and sets bit 4.
+ *   new_ids      device int32[num_blocks]: each block's new id (its own where
+ *                it stays), -1 for a free one.
+ *   copy_src, copy_dst  device int32[num_blocks / 2]: the moves in order, then
+ *                (-1, -1).
+ *   num_used     device int32[1]: U. */
+PAGEDKV_API int kv_compact_blocks(const int32_t *block_tables, const int32_t *ref_counts, int32_t *new_tables,
+                                  int32_t *new_ref_counts, int32_t *new_ids, int32_t *copy_src,
+                                  int32_t *copy_dst, int32_t *num_used, uint32_t max_blocks_per_seq,
+                                  uint32_t num_seqs, uint32_t num_blocks, void *stream);
+
+/* ------------------------------------------------------------------------
  * Split-KV workspace (not on the pages: flash-decoding partials and the
  * combine step need scratch). The caller allocates device memory of at
  * least kv_decode_workspace_bytes(...) for the largest decode it will run
@@ -383,7 +592,10 @@ PAGEDKV_API int kv_set_decode_workspace(void *device_ptr, size_t bytes);
  *          num_q_tokens (that sequence skipped)
  *   bit 3: (bounds-checking build only) a slot or block id outside the pool
  *          set by kv_debug_set_pool
- *   (bit 0 also covers the prefill pipeline and the fused K write's wait
+ *   bit 4: a page call (kv_copy_blocks to kv_compact_blocks) met an id, a row
+ *          or a count out of range (skipped)
+ *   bit 5: kv_fork_blocks found no free block for a fork (not made)
+ *   (bits 1 and 2 also cover kv_write_fp8_block; bit 0 also covers the prefill pipeline and the fused K write's wait
  *   for its shared-memory copy of the sin/cos table)
  * ---------------------------------------------------------------------- */
 PAGEDKV_API int kv_get_device_error(uint32_t *bits);

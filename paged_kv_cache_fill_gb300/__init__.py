@@ -25,6 +25,10 @@ __all__ = [
     "kv_write_fused_k_norm_rope_fp8", "kv_write_v_only", "paged_decode_attn_bf16",
     "paged_decode_attn_fp8k", "paged_decode_attn_fp8", "paged_prefill_attn_bf16", "paged_prefill_attn_fp8k",
     "paged_prefill_attn_fp8", "paged_decode_attn_fp8k_static_scratch",
+    "paged_decode_attn_bf16_sinks", "paged_decode_attn_fp8k_sinks", "paged_decode_attn_fp8_sinks",
+    "paged_prefill_attn_bf16_sinks", "paged_prefill_attn_fp8k_sinks", "paged_prefill_attn_fp8_sinks",
+    "kv_write_fp8_block", "paged_decode_attn_fp8_block", "paged_prefill_attn_fp8_block",
+    "kv_copy_blocks", "kv_free_blocks", "kv_free_window_blocks", "kv_fork_blocks", "kv_compact_blocks",
     "kv_decode_workspace_bytes",
     "kv_set_decode_workspace", "kv_get_device_error", "kv_device_info", "kv_debug_set_pool",
     "kv_debug_set_wait_limit", "use_library",
@@ -73,6 +77,20 @@ _SIGNATURES = {
     "paged_decode_attn_fp8k_static_scratch": (
         ctypes.c_int,
         [_P, _P, _P, _P, _P, _P, _U32, _U32, _U32, _U32, _U32, _U32, _F32, _F32, _U32, _U32, _P]),
+    "paged_decode_attn_bf16_sinks": (ctypes.c_int, [_P] * 6 + [_U32] * 6 + [_F32] + [_U32] * 3 + [_P]),
+    "paged_decode_attn_fp8k_sinks": (ctypes.c_int, [_P] * 6 + [_U32] * 6 + [_F32] * 2 + [_U32] * 3 + [_P]),
+    "paged_decode_attn_fp8_sinks": (ctypes.c_int, [_P] * 6 + [_U32] * 6 + [_F32] * 3 + [_U32] * 3 + [_P]),
+    "paged_prefill_attn_bf16_sinks": (ctypes.c_int, [_P] * 7 + [_U32] * 7 + [_F32] + [_U32] * 3 + [_P]),
+    "paged_prefill_attn_fp8k_sinks": (ctypes.c_int, [_P] * 7 + [_U32] * 7 + [_F32] * 2 + [_U32] * 3 + [_P]),
+    "paged_prefill_attn_fp8_sinks": (ctypes.c_int, [_P] * 7 + [_U32] * 7 + [_F32] * 3 + [_U32] * 3 + [_P]),
+    "kv_write_fp8_block": (ctypes.c_int, [_P] * 9 + [_U32] * 8 + [_P]),
+    "paged_decode_attn_fp8_block": (ctypes.c_int, [_P] * 8 + [_U32] * 6 + [_F32] + [_U32] * 3 + [_P]),
+    "paged_prefill_attn_fp8_block": (ctypes.c_int, [_P] * 9 + [_U32] * 7 + [_F32] + [_U32] * 3 + [_P]),
+    "kv_copy_blocks": (ctypes.c_int, [_P, _P, _U32, _P, _P, _U32, _U32, _P]),
+    "kv_free_blocks": (ctypes.c_int, [_P] * 4 + [_U32] * 3 + [_P]),
+    "kv_free_window_blocks": (ctypes.c_int, [_P] * 3 + [_U32] * 6 + [_P]),
+    "kv_fork_blocks": (ctypes.c_int, [_P] * 7 + [_U32] * 5 + [_P]),
+    "kv_compact_blocks": (ctypes.c_int, [_P] * 8 + [_U32] * 3 + [_P]),
     "kv_decode_workspace_bytes": (_SZ, [_U32, _U32, _U32, _U32, _U32, _U32]),
     "kv_set_decode_workspace": (ctypes.c_int, [_P, _SZ]),
     "kv_get_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
@@ -275,6 +293,153 @@ def paged_decode_attn_fp8k_static_scratch(q, k_cache_fp8, v_cache, output, block
         k_scale, q_stride, sliding_window, _stream(stream)))
 
 
+def paged_decode_attn_bf16_sinks(q, k_cache, v_cache, output, block_tables, seq_lens, max_blocks_per_seq,
+                                 num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d,
+                                 q_stride, sliding_window, num_sinks, stream=None):
+    """paged_decode_attn_bf16 with the first num_sinks positions visible under the window."""
+    _check("paged_decode_attn_bf16_sinks", lib().paged_decode_attn_bf16_sinks(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(output), _ptr(block_tables), _ptr(seq_lens),
+        max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, q_stride,
+        sliding_window, num_sinks, _stream(stream)))
+
+
+def paged_decode_attn_fp8k_sinks(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, max_blocks_per_seq,
+                                 num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale,
+                                 q_stride, sliding_window, num_sinks, stream=None):
+    """paged_decode_attn_fp8k with the first num_sinks positions visible under the window."""
+    _check("paged_decode_attn_fp8k_sinks", lib().paged_decode_attn_fp8k_sinks(
+        _ptr(q), _ptr(k_cache_fp8), _ptr(v_cache), _ptr(output), _ptr(block_tables), _ptr(seq_lens),
+        max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale,
+        q_stride, sliding_window, num_sinks, _stream(stream)))
+
+
+def paged_decode_attn_fp8_sinks(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
+                                num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale,
+                                v_scale, q_stride, sliding_window, num_sinks, stream=None):
+    """paged_decode_attn_fp8 with the first num_sinks positions visible under the window."""
+    _check("paged_decode_attn_fp8_sinks", lib().paged_decode_attn_fp8_sinks(
+        _ptr(q), _ptr(k_cache_fp8), _ptr(v_cache_fp8), _ptr(output), _ptr(block_tables), _ptr(seq_lens),
+        max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale,
+        v_scale, q_stride, sliding_window, num_sinks, _stream(stream)))
+
+
+def paged_prefill_attn_bf16_sinks(q, k_cache, v_cache, output, block_tables, seq_lens, query_start_loc,
+                                  max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads,
+                                  head_dim, block_size, inv_sqrt_d, q_stride, sliding_window, num_sinks,
+                                  stream=None):
+    """paged_prefill_attn_bf16 with sinks; `output` is BF16."""
+    _check("paged_prefill_attn_bf16_sinks", lib().paged_prefill_attn_bf16_sinks(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(output), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(query_start_loc), max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+        block_size, inv_sqrt_d, q_stride, sliding_window, num_sinks, _stream(stream)))
+
+
+def paged_prefill_attn_fp8k_sinks(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, query_start_loc,
+                                  max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads,
+                                  head_dim, block_size, inv_sqrt_d, k_scale, q_stride, sliding_window,
+                                  num_sinks, stream=None):
+    """paged_prefill_attn_fp8k with sinks; `output` is BF16."""
+    _check("paged_prefill_attn_fp8k_sinks", lib().paged_prefill_attn_fp8k_sinks(
+        _ptr(q), _ptr(k_cache_fp8), _ptr(v_cache), _ptr(output), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(query_start_loc), max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+        block_size, inv_sqrt_d, k_scale, q_stride, sliding_window, num_sinks, _stream(stream)))
+
+
+def paged_prefill_attn_fp8_sinks(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, query_start_loc,
+                                 max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads,
+                                 head_dim, block_size, inv_sqrt_d, k_scale, v_scale, q_stride, sliding_window,
+                                 num_sinks, stream=None):
+    """paged_prefill_attn_fp8 with sinks; `output` is BF16."""
+    _check("paged_prefill_attn_fp8_sinks", lib().paged_prefill_attn_fp8_sinks(
+        _ptr(q), _ptr(k_cache_fp8), _ptr(v_cache_fp8), _ptr(output), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(query_start_loc), max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+        block_size, inv_sqrt_d, k_scale, v_scale, q_stride, sliding_window, num_sinks, _stream(stream)))
+
+
+def kv_write_fp8_block(key, value, k_cache_fp8, v_cache_fp8, k_scales, v_scales, block_tables, seq_lens,
+                       query_start_loc, max_blocks_per_seq, num_seqs, num_tokens, num_kv_heads, head_dim,
+                       block_size, key_stride, value_stride, stream=None):
+    """Write each sequence's last tokens (those that query_start_loc counts) into
+    an E4M3 cache with one power-of-two float32 scale per (block, KV head)."""
+    _check("kv_write_fp8_block", lib().kv_write_fp8_block(
+        _ptr(key), _ptr(value), _ptr(k_cache_fp8), _ptr(v_cache_fp8), _ptr(k_scales), _ptr(v_scales),
+        _ptr(block_tables), _ptr(seq_lens), _ptr(query_start_loc), max_blocks_per_seq, num_seqs, num_tokens,
+        num_kv_heads, head_dim, block_size, key_stride, value_stride, _stream(stream)))
+
+
+def paged_decode_attn_fp8_block(q, k_cache_fp8, v_cache_fp8, k_scales, v_scales, output, block_tables, seq_lens,
+                                max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                inv_sqrt_d, q_stride, sliding_window, num_sinks, stream=None):
+    """Paged decode, with sinks, over the cache that kv_write_fp8_block fills."""
+    _check("paged_decode_attn_fp8_block", lib().paged_decode_attn_fp8_block(
+        _ptr(q), _ptr(k_cache_fp8), _ptr(v_cache_fp8), _ptr(k_scales), _ptr(v_scales), _ptr(output),
+        _ptr(block_tables), _ptr(seq_lens), max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, head_dim,
+        block_size, inv_sqrt_d, q_stride, sliding_window, num_sinks, _stream(stream)))
+
+
+def paged_prefill_attn_fp8_block(q, k_cache_fp8, v_cache_fp8, k_scales, v_scales, output, block_tables,
+                                 seq_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_q_tokens,
+                                 num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, q_stride,
+                                 sliding_window, num_sinks, stream=None):
+    """Chunked prefill, with sinks, over that cache; `output` is BF16."""
+    _check("paged_prefill_attn_fp8_block", lib().paged_prefill_attn_fp8_block(
+        _ptr(q), _ptr(k_cache_fp8), _ptr(v_cache_fp8), _ptr(k_scales), _ptr(v_scales), _ptr(output),
+        _ptr(block_tables), _ptr(seq_lens), _ptr(query_start_loc), max_blocks_per_seq, num_seqs, num_q_tokens,
+        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, q_stride, sliding_window, num_sinks,
+        _stream(stream)))
+
+
+def kv_copy_blocks(pools, src_blocks, dst_blocks, num_pairs, num_blocks, stream=None):
+    """Copy block src_blocks[i] to dst_blocks[i] in every one of `pools`, a
+    sequence of tensors of num_blocks blocks each (every layer's caches and
+    scales). Pairs with a negative id are padding."""
+    n = len(pools)
+    bases, sizes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)()
+    for i, t in enumerate(pools):
+        bases[i] = _ptr(t)
+        nbytes = t.numel() * t.element_size()
+        if num_blocks <= 0 or nbytes % num_blocks:
+            raise ValueError(f"pool {i} does not hold {num_blocks} equal blocks")
+        sizes[i] = nbytes // num_blocks
+    _check("kv_copy_blocks", lib().kv_copy_blocks(
+        bases, sizes, n, _ptr(src_blocks), _ptr(dst_blocks), num_pairs, num_blocks, _stream(stream)))
+
+
+def kv_free_blocks(block_tables, ref_counts, first_block, end_block, max_blocks_per_seq, num_seqs, num_blocks,
+                   stream=None):
+    """Release entries [first_block[s], end_block[s]) of every row s."""
+    _check("kv_free_blocks", lib().kv_free_blocks(
+        _ptr(block_tables), _ptr(ref_counts), _ptr(first_block), _ptr(end_block), max_blocks_per_seq, num_seqs,
+        num_blocks, _stream(stream)))
+
+
+def kv_free_window_blocks(block_tables, ref_counts, seq_lens, max_blocks_per_seq, num_seqs, num_blocks,
+                          block_size, sliding_window, num_sinks, stream=None):
+    """Release the blocks that a sliding window with sinks has left behind."""
+    _check("kv_free_window_blocks", lib().kv_free_window_blocks(
+        _ptr(block_tables), _ptr(ref_counts), _ptr(seq_lens), max_blocks_per_seq, num_seqs, num_blocks,
+        block_size, sliding_window, num_sinks, _stream(stream)))
+
+
+def kv_fork_blocks(block_tables, seq_lens, ref_counts, src_seqs, dst_seqs, copy_src, copy_dst, num_forks,
+                   max_blocks_per_seq, num_seqs, num_blocks, block_size, stream=None):
+    """Make rows dst_seqs forks of rows src_seqs: full blocks shared, a partial
+    one given a free block and a (copy_src, copy_dst) pair for kv_copy_blocks."""
+    _check("kv_fork_blocks", lib().kv_fork_blocks(
+        _ptr(block_tables), _ptr(seq_lens), _ptr(ref_counts), _ptr(src_seqs), _ptr(dst_seqs), _ptr(copy_src),
+        _ptr(copy_dst), num_forks, max_blocks_per_seq, num_seqs, num_blocks, block_size, _stream(stream)))
+
+
+def kv_compact_blocks(block_tables, ref_counts, new_tables, new_ref_counts, new_ids, copy_src, copy_dst,
+                      num_used, max_blocks_per_seq, num_seqs, num_blocks, stream=None):
+    """Move the blocks in use to the lowest ids: new tables, counts and ids, and
+    the moves for kv_copy_blocks."""
+    _check("kv_compact_blocks", lib().kv_compact_blocks(
+        _ptr(block_tables), _ptr(ref_counts), _ptr(new_tables), _ptr(new_ref_counts), _ptr(new_ids),
+        _ptr(copy_src), _ptr(copy_dst), _ptr(num_used), max_blocks_per_seq, num_seqs, num_blocks,
+        _stream(stream)))
+
+
 def kv_decode_workspace_bytes(max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, head_dim,
                               block_size) -> int:
     return int(lib().kv_decode_workspace_bytes(max_blocks_per_seq, num_seqs, num_q_heads,
@@ -314,7 +479,9 @@ def kv_get_device_error() -> int:
     fault bits: 1 = a pipeline wait timed out, 2 = a sequence length was
     clamped to its block table, 4 = a prefill's query_start_loc was
     decreasing, negative or past num_q_tokens (that sequence skipped),
-    8 = (bounds-checking build) a slot or block id outside the pool."""
+    8 = (bounds-checking build) a slot or block id outside the pool, 16 = a
+    page call met an id, row or count out of range, 32 = a fork found no free
+    block."""
     bits = ctypes.c_uint32(0)
     status = lib().kv_get_device_error(ctypes.byref(bits))
     if status != KV_ERR_DEVICE:  # KV_ERR_DEVICE only says that some bit was set

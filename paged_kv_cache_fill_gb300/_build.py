@@ -22,7 +22,8 @@ OUT_DIR = os.path.join(CSRC, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
 OUT_DIR_DEBUG = os.path.join(CSRC, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libpagedkv_debug.so")
-SOURCES = ["abi.cu", "kv_write.cu", "fused_k.cu", "decode.cu", "prefill.cu", "static_scratch.cu"]
+SOURCES = ["abi.cu", "kv_write.cu", "fused_k.cu", "decode.cu", "prefill.cu", "static_scratch.cu",
+           "block_write.cu", "pages.cu"]
 HEADERS = ["common.cuh", "internal.h", "rope_tables.h", os.path.join("..", "..", "include", "pagedkv.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

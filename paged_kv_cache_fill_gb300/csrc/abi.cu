@@ -195,9 +195,11 @@ static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_
                          const int32_t* block_tables, const int32_t* seq_lens, uint32_t max_blocks_per_seq,
                          uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_dim,
                          uint32_t block_size, float inv_sqrt_d, float k_scale, uint32_t q_stride,
-                         uint32_t sliding_window, bool fp8, bool fp8_v, float v_scale, void* stream) {
+                         uint32_t sliding_window, bool fp8, bool fp8_v, float v_scale, uint32_t num_sinks,
+                         bool block_scales, const float* k_scales, const float* v_scales, void* stream) {
   if (num_seqs == 0) return KV_OK;
   if (!q || !k_cache || !v_cache || !output || !block_tables || !seq_lens) return KV_ERR_INVALID_ARG;
+  if (block_scales && (!k_scales || !v_scales)) return KV_ERR_INVALID_ARG;
   if (num_kv_heads == 0 || num_q_heads == 0 || num_q_heads % num_kv_heads) return KV_ERR_INVALID_ARG;
   if (head_dim == 0 || block_size == 0) return KV_ERR_INVALID_ARG;
   if (uint64_t(q_stride) < uint64_t(num_q_heads) * head_dim) return KV_ERR_INVALID_ARG;
@@ -235,6 +237,9 @@ static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_
   a.fp8 = fp8;
   a.fp8_v = fp8_v;
   a.v_scale = v_scale;
+  a.num_sinks = num_sinks;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
   {
     std::lock_guard<std::mutex> lock(g_mutex);
     a.workspace = g_ws_ptr[dev.device];
@@ -258,7 +263,7 @@ int paged_decode_attn_bf16(const kv_bf16_t* q, const kv_bf16_t* k_cache, const k
                            uint32_t q_stride, uint32_t sliding_window, void* stream) {
   return decode_common(q, k_cache, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
-                       sliding_window, false, false, 1.0f, stream);
+                       sliding_window, false, false, 1.0f, 0, false, nullptr, nullptr, stream);
 }
 
 int paged_decode_attn_fp8k(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_bf16_t* v_cache,
@@ -268,7 +273,7 @@ int paged_decode_attn_fp8k(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, con
                            float k_scale, uint32_t q_stride, uint32_t sliding_window, void* stream) {
   return decode_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, false, 1.0f, stream);
+                       sliding_window, true, false, 1.0f, 0, false, nullptr, nullptr, stream);
 }
 
 int paged_decode_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
@@ -279,18 +284,63 @@ int paged_decode_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, cons
                           void* stream) {
   return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, true, v_scale, stream);
+                       sliding_window, true, true, v_scale, 0, false, nullptr, nullptr, stream);
 }
 
-static int prefill_common(const kv_bf16_t* q, const void* k_cache, const void* v_cache, float* output,
+int paged_decode_attn_bf16_sinks(const kv_bf16_t* q, const kv_bf16_t* k_cache, const kv_bf16_t* v_cache,
+                                 float* output, const int32_t* block_tables, const int32_t* seq_lens,
+                                 uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_heads,
+                                 uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size, float inv_sqrt_d,
+                                 uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks, void* stream) {
+  return decode_common(q, k_cache, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
+                       sliding_window, false, false, 1.0f, num_sinks, false, nullptr, nullptr, stream);
+}
+
+int paged_decode_attn_fp8k_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_bf16_t* v_cache,
+                                 float* output, const int32_t* block_tables, const int32_t* seq_lens,
+                                 uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_heads,
+                                 uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size, float inv_sqrt_d,
+                                 float k_scale, uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks,
+                                 void* stream) {
+  return decode_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
+                       sliding_window, true, false, 1.0f, num_sinks, false, nullptr, nullptr, stream);
+}
+
+int paged_decode_attn_fp8_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
+                                float* output, const int32_t* block_tables, const int32_t* seq_lens,
+                                uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_heads,
+                                uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size, float inv_sqrt_d,
+                                float k_scale, float v_scale, uint32_t q_stride, uint32_t sliding_window,
+                                uint32_t num_sinks, void* stream) {
+  return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
+                       num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
+                       sliding_window, true, true, v_scale, num_sinks, false, nullptr, nullptr, stream);
+}
+
+int paged_decode_attn_fp8_block(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
+                                const float* k_scales, const float* v_scales, float* output,
+                                const int32_t* block_tables, const int32_t* seq_lens, uint32_t max_blocks_per_seq,
+                                uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_dim,
+                                uint32_t block_size, float inv_sqrt_d, uint32_t q_stride, uint32_t sliding_window,
+                                uint32_t num_sinks, void* stream) {
+  return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
+                       num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
+                       sliding_window, true, true, 1.0f, num_sinks, true, k_scales, v_scales, stream);
+}
+
+static int prefill_common(const kv_bf16_t* q, const void* k_cache, const void* v_cache, void* output,
                           const int32_t* block_tables, const int32_t* seq_lens, const int32_t* query_start_loc,
                           uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_tokens,
                           uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size,
                           float inv_sqrt_d, float k_scale, float v_scale, uint32_t q_stride,
-                          uint32_t sliding_window, bool fp8, bool fp8_v, void* stream) {
+                          uint32_t sliding_window, bool fp8, bool fp8_v, bool bf16_out, uint32_t num_sinks,
+                          bool block_scales, const float* k_scales, const float* v_scales, void* stream) {
   if (num_seqs == 0 || num_q_tokens == 0) return KV_OK;
   if (!q || !k_cache || !v_cache || !output || !block_tables || !seq_lens || !query_start_loc)
     return KV_ERR_INVALID_ARG;
+  if (block_scales && (!k_scales || !v_scales)) return KV_ERR_INVALID_ARG;
   if (num_kv_heads == 0 || num_q_heads == 0 || num_q_heads % num_kv_heads) return KV_ERR_INVALID_ARG;
   if (head_dim == 0 || block_size == 0) return KV_ERR_INVALID_ARG;
   if (uint64_t(q_stride) < uint64_t(num_q_heads) * head_dim) return KV_ERR_INVALID_ARG;
@@ -329,6 +379,10 @@ static int prefill_common(const kv_bf16_t* q, const void* k_cache, const void* v
   a.sliding_window = sliding_window;
   a.fp8 = fp8;
   a.fp8_v = fp8_v;
+  a.bf16_out = bf16_out;
+  a.num_sinks = num_sinks;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
   return launch_prefill(a, as_stream(stream));
 }
 
@@ -339,7 +393,7 @@ int paged_prefill_attn_bf16(const kv_bf16_t* q, const kv_bf16_t* k_cache, const 
                             float inv_sqrt_d, uint32_t q_stride, uint32_t sliding_window, void* stream) {
   return prefill_common(q, k_cache, v_cache, output, block_tables, seq_lens, query_start_loc, max_blocks_per_seq,
                         num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f,
-                        1.0f, q_stride, sliding_window, false, false, stream);
+                        1.0f, q_stride, sliding_window, false, false, false, 0, false, nullptr, nullptr, stream);
 }
 
 int paged_prefill_attn_fp8k(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_bf16_t* v_cache,
@@ -350,7 +404,8 @@ int paged_prefill_attn_fp8k(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, co
                             uint32_t sliding_window, void* stream) {
   return prefill_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, query_start_loc,
                         max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
-                        inv_sqrt_d, k_scale, 1.0f, q_stride, sliding_window, true, false, stream);
+                        inv_sqrt_d, k_scale, 1.0f, q_stride, sliding_window, true, false, false, 0, false, nullptr,
+                        nullptr, stream);
 }
 
 int paged_prefill_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
@@ -361,7 +416,174 @@ int paged_prefill_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, con
                            uint32_t sliding_window, void* stream) {
   return prefill_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, query_start_loc,
                         max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
-                        inv_sqrt_d, k_scale, v_scale, q_stride, sliding_window, true, true, stream);
+                        inv_sqrt_d, k_scale, v_scale, q_stride, sliding_window, true, true, false, 0, false, nullptr,
+                        nullptr, stream);
+}
+
+// The scores' maximum is taken before the scale is applied, so the calls that
+// say so want a positive one.
+static bool positive(float x) { return x > 0.0f && isfinite(x); }
+
+int paged_prefill_attn_bf16_sinks(const kv_bf16_t* q, const kv_bf16_t* k_cache, const kv_bf16_t* v_cache,
+                                  kv_bf16_t* output, const int32_t* block_tables, const int32_t* seq_lens,
+                                  const int32_t* query_start_loc, uint32_t max_blocks_per_seq, uint32_t num_seqs,
+                                  uint32_t num_q_tokens, uint32_t num_q_heads, uint32_t num_kv_heads,
+                                  uint32_t head_dim, uint32_t block_size, float inv_sqrt_d, uint32_t q_stride,
+                                  uint32_t sliding_window, uint32_t num_sinks, void* stream) {
+  if (num_seqs && num_q_tokens && !positive(inv_sqrt_d)) return KV_ERR_INVALID_ARG;
+  return prefill_common(q, k_cache, v_cache, output, block_tables, seq_lens, query_start_loc, max_blocks_per_seq,
+                        num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f,
+                        1.0f, q_stride, sliding_window, false, false, true, num_sinks, false, nullptr, nullptr,
+                        stream);
+}
+
+int paged_prefill_attn_fp8k_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_bf16_t* v_cache,
+                                  kv_bf16_t* output, const int32_t* block_tables, const int32_t* seq_lens,
+                                  const int32_t* query_start_loc, uint32_t max_blocks_per_seq, uint32_t num_seqs,
+                                  uint32_t num_q_tokens, uint32_t num_q_heads, uint32_t num_kv_heads,
+                                  uint32_t head_dim, uint32_t block_size, float inv_sqrt_d, float k_scale,
+                                  uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks, void* stream) {
+  if (num_seqs && num_q_tokens && !positive(inv_sqrt_d)) return KV_ERR_INVALID_ARG;
+  return prefill_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, query_start_loc,
+                        max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                        inv_sqrt_d, k_scale, 1.0f, q_stride, sliding_window, true, false, true, num_sinks, false,
+                        nullptr, nullptr, stream);
+}
+
+int paged_prefill_attn_fp8_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
+                                 kv_bf16_t* output, const int32_t* block_tables, const int32_t* seq_lens,
+                                 const int32_t* query_start_loc, uint32_t max_blocks_per_seq, uint32_t num_seqs,
+                                 uint32_t num_q_tokens, uint32_t num_q_heads, uint32_t num_kv_heads,
+                                 uint32_t head_dim, uint32_t block_size, float inv_sqrt_d, float k_scale,
+                                 float v_scale, uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks,
+                                 void* stream) {
+  if (num_seqs && num_q_tokens && !positive(inv_sqrt_d)) return KV_ERR_INVALID_ARG;
+  return prefill_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, query_start_loc,
+                        max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                        inv_sqrt_d, k_scale, v_scale, q_stride, sliding_window, true, true, true, num_sinks, false,
+                        nullptr, nullptr, stream);
+}
+
+int paged_prefill_attn_fp8_block(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
+                                 const float* k_scales, const float* v_scales, kv_bf16_t* output,
+                                 const int32_t* block_tables, const int32_t* seq_lens,
+                                 const int32_t* query_start_loc, uint32_t max_blocks_per_seq, uint32_t num_seqs,
+                                 uint32_t num_q_tokens, uint32_t num_q_heads, uint32_t num_kv_heads,
+                                 uint32_t head_dim, uint32_t block_size, float inv_sqrt_d, uint32_t q_stride,
+                                 uint32_t sliding_window, uint32_t num_sinks, void* stream) {
+  if (num_seqs && num_q_tokens && !positive(inv_sqrt_d)) return KV_ERR_INVALID_ARG;
+  return prefill_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, query_start_loc,
+                        max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                        inv_sqrt_d, 1.0f, 1.0f, q_stride, sliding_window, true, true, true, num_sinks, true, k_scales,
+                        v_scales, stream);
+}
+
+int kv_write_fp8_block(const kv_bf16_t* key, const kv_bf16_t* value, kv_e4m3_t* k_cache_fp8, kv_e4m3_t* v_cache_fp8,
+                       float* k_scales, float* v_scales, const int32_t* block_tables, const int32_t* seq_lens,
+                       const int32_t* query_start_loc, uint32_t max_blocks_per_seq, uint32_t num_seqs,
+                       uint32_t num_tokens, uint32_t num_kv_heads, uint32_t head_dim, uint32_t block_size,
+                       uint32_t key_stride, uint32_t value_stride, void* stream) {
+  if (num_tokens == 0 || num_seqs == 0) return KV_OK;
+  if (!key || !value || !k_cache_fp8 || !v_cache_fp8 || !k_scales || !v_scales || !block_tables || !seq_lens ||
+      !query_start_loc)
+    return KV_ERR_INVALID_ARG;
+  if (int r = check_rows(num_kv_heads, head_dim, block_size)) return r;
+  const uint32_t row = num_kv_heads * head_dim;
+  if (key_stride < row || value_stride < row) return KV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return KV_ERR_UNSUPPORTED;
+  if (!is_pow2(block_size) || block_size < 16 || block_size > 256) return KV_ERR_UNSUPPORTED;
+  if (!aligned(k_cache_fp8, 16) || !aligned(v_cache_fp8, 16)) return KV_ERR_UNSUPPORTED;
+  if (uint64_t(max_blocks_per_seq) * block_size >= (1ull << 31) || num_tokens >= (1u << 31))
+    return KV_ERR_UNSUPPORTED;
+  if (device_info().device < 0) return KV_ERR_CUDA;
+  BlockWriteArgs a{};
+  a.key = key;
+  a.value = value;
+  a.k_cache = k_cache_fp8;
+  a.v_cache = v_cache_fp8;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.query_start_loc = query_start_loc;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  return launch_write_fp8_block(a, as_stream(stream));
+}
+
+int kv_copy_blocks(void* const* pools, const size_t* block_bytes, uint32_t num_pools, const int32_t* src_blocks,
+                   const int32_t* dst_blocks, uint32_t num_pairs, uint32_t num_blocks, void* stream) {
+  if (num_pools == 0 || num_pairs == 0) return KV_OK;
+  if (!pools || !block_bytes || !src_blocks || !dst_blocks || num_blocks == 0) return KV_ERR_INVALID_ARG;
+  for (uint32_t i = 0; i < num_pools; ++i) {
+    if (!pools[i] || block_bytes[i] == 0) return KV_ERR_INVALID_ARG;
+    if (block_bytes[i] >= (size_t(1) << 40)) return KV_ERR_UNSUPPORTED;
+  }
+  if (num_blocks >= (1u << 31) || num_pairs >= (1u << 31)) return KV_ERR_UNSUPPORTED;
+  return launch_copy_blocks(pools, block_bytes, num_pools, src_blocks, dst_blocks, num_pairs, num_blocks,
+                            as_stream(stream));
+}
+
+// Shared checks of the calls on block tables and reference counts.
+static int check_pages(uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks) {
+  if (max_blocks_per_seq == 0 || num_blocks == 0) return KV_ERR_INVALID_ARG;
+  if (num_blocks >= (1u << 31) || max_blocks_per_seq >= (1u << 31) || num_seqs >= (1u << 31))
+    return KV_ERR_UNSUPPORTED;
+  return KV_OK;
+}
+
+int kv_free_blocks(int32_t* block_tables, int32_t* ref_counts, const int32_t* first_block, const int32_t* end_block,
+                   uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks, void* stream) {
+  if (num_seqs == 0) return KV_OK;
+  if (!block_tables || !ref_counts || !first_block || !end_block) return KV_ERR_INVALID_ARG;
+  if (int r = check_pages(max_blocks_per_seq, num_seqs, num_blocks)) return r;
+  return from_cuda(launch_free_blocks(block_tables, ref_counts, first_block, end_block, nullptr, max_blocks_per_seq,
+                                      num_seqs, num_blocks, 1, 0, 0, as_stream(stream)));
+}
+
+int kv_free_window_blocks(int32_t* block_tables, int32_t* ref_counts, const int32_t* seq_lens,
+                          uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks, uint32_t block_size,
+                          uint32_t sliding_window, uint32_t num_sinks, void* stream) {
+  if (num_seqs == 0 || sliding_window == 0) return KV_OK;  // without a window nothing is left behind
+  if (!block_tables || !ref_counts || !seq_lens || block_size == 0) return KV_ERR_INVALID_ARG;
+  if (int r = check_pages(max_blocks_per_seq, num_seqs, num_blocks)) return r;
+  return from_cuda(launch_free_blocks(block_tables, ref_counts, nullptr, nullptr, seq_lens, max_blocks_per_seq,
+                                      num_seqs, num_blocks, block_size, sliding_window, num_sinks,
+                                      as_stream(stream)));
+}
+
+int kv_fork_blocks(int32_t* block_tables, int32_t* seq_lens, int32_t* ref_counts, const int32_t* src_seqs,
+                   const int32_t* dst_seqs, int32_t* copy_src, int32_t* copy_dst, uint32_t num_forks,
+                   uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks, uint32_t block_size,
+                   void* stream) {
+  if (num_forks == 0) return KV_OK;
+  if (!block_tables || !seq_lens || !ref_counts || !src_seqs || !dst_seqs || !copy_src || !copy_dst ||
+      num_seqs == 0 || block_size == 0)
+    return KV_ERR_INVALID_ARG;
+  if (int r = check_pages(max_blocks_per_seq, num_seqs, num_blocks)) return r;
+  if (!aligned(ref_counts, 16) || num_forks >= (1u << 31)) return KV_ERR_UNSUPPORTED;
+  return launch_fork_blocks(block_tables, seq_lens, ref_counts, src_seqs, dst_seqs, copy_src, copy_dst, num_forks,
+                            max_blocks_per_seq, num_seqs, num_blocks, block_size, as_stream(stream));
+}
+
+int kv_compact_blocks(const int32_t* block_tables, const int32_t* ref_counts, int32_t* new_tables,
+                      int32_t* new_ref_counts, int32_t* new_ids, int32_t* copy_src, int32_t* copy_dst,
+                      int32_t* num_used, uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks,
+                      void* stream) {
+  if (num_blocks == 0) return KV_OK;
+  if (!ref_counts || !new_ref_counts || !new_ids || !num_used) return KV_ERR_INVALID_ARG;
+  if (num_blocks > 1 && (!copy_src || !copy_dst)) return KV_ERR_INVALID_ARG;
+  if (num_seqs && (!block_tables || !new_tables)) return KV_ERR_INVALID_ARG;
+  if (int r = check_pages(num_seqs ? max_blocks_per_seq : 1, num_seqs, num_blocks)) return r;
+  return from_cuda(launch_compact_blocks(block_tables, ref_counts, new_tables, new_ref_counts, new_ids, copy_src,
+                                         copy_dst, num_used, max_blocks_per_seq, num_seqs, num_blocks,
+                                         as_stream(stream)));
 }
 
 size_t kv_decode_workspace_bytes(uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_heads,
@@ -383,18 +605,21 @@ int kv_set_decode_workspace(void* device_ptr, size_t bytes) {
 int kv_get_device_error(uint32_t* bits) {
   if (!bits) return KV_ERR_INVALID_ARG;
   if (cudaDeviceSynchronize() != cudaSuccess) return KV_ERR_CUDA;
-  uint32_t decode_bits = 0, prefill_bits = 0, fused_bits = 0;
+  uint32_t decode_bits = 0, prefill_bits = 0, fused_bits = 0, block_write_bits = 0, pages_bits = 0;
   if (read_and_clear_decode_error(&decode_bits) != cudaSuccess ||
       read_and_clear_prefill_error(&prefill_bits) != cudaSuccess ||
-      read_and_clear_fused_error(&fused_bits) != cudaSuccess)
+      read_and_clear_fused_error(&fused_bits) != cudaSuccess ||
+      read_and_clear_block_write_error(&block_write_bits) != cudaSuccess ||
+      read_and_clear_pages_error(&pages_bits) != cudaSuccess)
     return KV_ERR_CUDA;
-  *bits = decode_bits | prefill_bits | fused_bits;
+  *bits = decode_bits | prefill_bits | fused_bits | block_write_bits | pages_bits;
 #ifdef PAGEDKV_DEBUG_BOUNDS
-  uint32_t d[4] = {0, 0, 0, 0};
+  uint32_t d[5] = {0, 0, 0, 0, 0};
   if (debug_read_and_clear_kv_write(&d[0]) != cudaSuccess || debug_read_and_clear_fused_k(&d[1]) != cudaSuccess ||
-      debug_read_and_clear_decode(&d[2]) != cudaSuccess || debug_read_and_clear_prefill(&d[3]) != cudaSuccess)
+      debug_read_and_clear_decode(&d[2]) != cudaSuccess || debug_read_and_clear_prefill(&d[3]) != cudaSuccess ||
+      debug_read_and_clear_block_write(&d[4]) != cudaSuccess)
     return KV_ERR_CUDA;
-  *bits |= d[0] | d[1] | d[2] | d[3];
+  *bits |= d[0] | d[1] | d[2] | d[3] | d[4];
 #endif
   return *bits ? KV_ERR_DEVICE : KV_OK;
 }
@@ -406,7 +631,8 @@ int kv_debug_set_pool(uint32_t num_blocks, uint32_t block_size) {
   if (debug_set_pool_kv_write(num_blocks, block_size) != cudaSuccess ||
       debug_set_pool_fused_k(num_blocks, block_size) != cudaSuccess ||
       debug_set_pool_decode(num_blocks, block_size) != cudaSuccess ||
-      debug_set_pool_prefill(num_blocks, block_size) != cudaSuccess)
+      debug_set_pool_prefill(num_blocks, block_size) != cudaSuccess ||
+      debug_set_pool_block_write(num_blocks, block_size) != cudaSuccess)
     return KV_ERR_CUDA;
   return KV_OK;
 #else

@@ -16,6 +16,8 @@ enum : uint32_t {
   kErrSeqLenClamped = 1u << 1,
   kErrQueryLayout = 1u << 2,
   kErrIndexOutOfPool = 1u << 3,  // bounds-checking build only
+  kErrPageRange = 1u << 4,       // page calls: an id, row or count out of range
+  kErrNoFreeBlock = 1u << 5,     // kv_fork_blocks: the pool is full
 };
 
 // How long a pipeline wait on an mbarrier may take before the kernel gives
@@ -151,6 +153,16 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
           smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+// 4-byte asynchronous copy global -> shared by one thread, and the thread's
+// arrival on `bar` once all such copies it has issued have landed (the arrival
+// is one of the count the barrier was initialised with).
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // ---------------------------------------------------------------- fragments

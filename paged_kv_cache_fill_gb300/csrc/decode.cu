@@ -1,5 +1,7 @@
 // Paged decode attention over a BF16, FP8-E4M3-K / BF16-V or FP8 K+V paged
-// cache.
+// cache, the FP8 K+V one with scalar scales or with one scale for each block
+// and KV head; full, sliding-window, or sliding-window with the first
+// num_sinks positions always visible.
 //
 // [kv_cache.rs] `paged_decode_attn_fp8` doc (one query per (query head,
 // sequence), block_tables i32[num_seqs * max_blocks_per_seq], seq_lens
@@ -37,6 +39,17 @@
 //     gives each lane two tokens of two adjacent dims; P then enters as f16
 //     hi + lo parts scaled by 2^8 (keeping small weights out of the f16
 //     subnormal range), and v_scale / 2^8 is applied at the end.
+//   * Block scales (kBlk): a tile lies in one cache block, so its K scale ks
+//     and V scale vs are one number each per head. The producer's lanes copy
+//     them next to the tile (4-byte cp.async, completing on the same
+//     barrier: a load into registers would stall the loader for a memory
+//     latency per block). ks multiplies the tile's scores. vs = 2^e m (1 <= m
+//     < 2) enters the weights under a second running maximum M' = max(z +
+//     e): acc = sum 2^(z + e - M') m code, l = sum 2^(z - M), so that the
+//     f16 weights keep their precision whatever the scales are, and the
+//     output is acc 2^(M' - M) / l.
+//   * Sinks: a sequence's tile list is its sink tiles followed by its window
+//     tiles; everything else sees one list of consecutive tile numbers.
 //   * Split-KV (flash-decoding): the pieces of a sequence cut by chunk
 //     boundaries write unnormalised partial outputs with their running max
 //     and sum to a caller-provided workspace; a combine kernel merges them in
@@ -87,6 +100,9 @@ struct DecodeParams {
   uint32_t heads_per_item;  // HG
   uint32_t num_head_groups;
   uint32_t q_stride, sliding_window;
+  int32_t num_sinks;          // first positions that stay visible under a window
+  const float* k_scales;      // kBlk: [num_blocks, num_kv_heads]
+  const float* v_scales;
   uint32_t max_splits;  // 0: no workspace, one item per (sequence, head group)
   uint32_t min_chunk_tiles;  // chunks at least this long keep every sequence within max_splits pieces
   float score_scale;    // inv_sqrt_d * log2(e)   (times k_scale for FP8)
@@ -95,8 +111,12 @@ struct DecodeParams {
 };
 
 // -------------------------------------------------------------- item walk
+// Positions [start, len) and, below start, [0, num_sinks): ntiles tiles, the
+// first ns of them the sink tiles 0.., the others t0... (A tile that holds
+// both sinks and window positions is t0.)
 struct SeqSpan {
-  int32_t len, start, t0, ntiles;
+  int32_t len, start, t0, ns, ntiles;
+  __device__ __forceinline__ int32_t tile(int32_t i) const { return i < ns ? i : i - ns + t0; }
 };
 
 __device__ __forceinline__ SeqSpan seq_span(int32_t raw_len, const DecodeParams& p) {
@@ -112,7 +132,9 @@ __device__ __forceinline__ SeqSpan seq_span(int32_t raw_len, const DecodeParams&
                 ? int32_t(int64_t(L) - int64_t(p.sliding_window))
                 : 0;
   s.t0 = s.start / kTile;
-  s.ntiles = L > 0 ? (L + kTile - 1) / kTile - s.t0 : 0;
+  const int32_t sinks = p.num_sinks < s.start ? p.num_sinks : s.start;
+  s.ns = (sinks + kTile - 1) / kTile < s.t0 ? (sinks + kTile - 1) / kTile : s.t0;
+  s.ntiles = L > 0 ? (L + kTile - 1) / kTile - s.t0 + s.ns : 0;
   return s;
 }
 
@@ -235,7 +257,9 @@ __device__ __forceinline__ void pv_tile(float (&acc)[D / 16][4], uint32_t vbase,
 template <bool kFp8V, int D, int NT>
 constexpr bool two_ctas_per_sm() { return kFp8V && D <= 128 && NT == 1; }
 
-template <bool kFp8, bool kFp8V, int D, int NT>
+constexpr uint32_t kMaxItemHeads = 8;  // heads per item, at most (geometry)
+
+template <bool kFp8, bool kFp8V, bool kBlk, int D, int NT>
 __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const DecodeParams p) {
@@ -245,12 +269,15 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   constexpr int kKCoord = kKRow >= 128 ? kKRow / 128 : 1;
   constexpr int kVCoord = kVRow >= 128 ? kVRow / 128 : 1;
   static_assert(kFp8 || !kFp8V, "an FP8 V cache comes with an FP8 K cache");
+  static_assert(kFp8V || !kBlk, "block scales come with an FP8 K and V cache");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * p.stage_bytes);
   uint64_t* empty = full + p.stages;
   StageMeta* meta = reinterpret_cast<StageMeta*>(empty + p.stages);
+  // kBlk: a stage's K scales of the item's heads, then its V scales
+  float* scales = reinterpret_cast<float*>(meta + p.stages);
   __shared__ uint64_t s_chunk, s_total;
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -259,7 +286,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kBlk ? 1 + 32 : 1);  // kBlk: and the producer's lanes, for the scales
       mbar_init(&empty[s], num_consumers);
     }
     fence_mbar_init();
@@ -296,9 +323,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
     // consumers wait on for that fill: drained before the CTA exits.
     uint32_t issued = 0, issued_parity = 0;
 
-    // One piece: tiles [tile_begin, tile_end) of sequence s for head group
-    // hg, the split'th piece of that pair (no tiles: one meta-only stage
-    // tells the consumers to write zeros).
+    // One piece: tiles [tile_begin, tile_end) of sequence s's tile list for
+    // head group hg, the split'th piece of that pair (no tiles: one meta-only
+    // stage tells the consumers to write zeros).
     auto emit = [&](uint32_t s, uint32_t hg, uint32_t split, const SeqSpan& span, int32_t tile_begin,
                     int32_t tile_end, int32_t base_flags) {
       const uint32_t heads_here = (hg + 1) * p.heads_per_item <= p.num_kv_heads
@@ -317,6 +344,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (kBlk && ok) mbar_arrive(&full[stage]);
         if (++stage == p.stages) { stage = 0; phase ^= 1; }
         return;
       }
@@ -324,7 +352,8 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       const int32_t tiles_per_block_shift = int32_t(p.block_shift) - 4;  // block_size >= 16
       int32_t cached_first_block = -1;  // first logical block held by the lanes
       int32_t cached_block_id = 0;
-      for (int32_t tile = tile_begin; tile < tile_end && ok; ++tile) {
+      for (int32_t i = tile_begin; i < tile_end && ok; ++i) {
+        const int32_t tile = span.tile(i);
         const int32_t lblock = tile >> tiles_per_block_shift;
         if (cached_first_block < 0 || lblock >= cached_first_block + 32) {
           cached_first_block = lblock;
@@ -337,8 +366,8 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           if (ok) {
             issued &= ~(1u << stage);
             int32_t flags = base_flags;
-            if (tile == tile_begin) flags |= kFirst;
-            if (tile == tile_end - 1) flags |= kLast;
+            if (i == tile_begin) flags |= kFirst;
+            if (i == tile_end - 1) flags |= kLast;
             meta[stage] = StageMeta{int32_t(s), int32_t(hg), int32_t(split), tile, span.start,
                                     span.len, flags, 0};
             // one box per tensor covers all heads of the piece (chunks past
@@ -362,6 +391,27 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
+        if constexpr (kBlk) {
+          // lanes 0.. the K scales of the piece's heads, lanes 16.. the V
+          // scales; every lane arrives once its copy (if any) has landed. A
+          // negative id (outside the caller's contract; the tile load fills
+          // zeros) takes block 0's scales.
+          __syncwarp();
+          if (ok) {
+            const uint32_t l = lane & 15;
+            if (l < heads_here) {
+#ifdef PAGEDKV_DEBUG_BOUNDS
+              const int32_t bid = block_id > 0 && dbg_block_ok(block_id) ? block_id : 0;
+#else
+              const int32_t bid = block_id > 0 ? block_id : 0;
+#endif
+              const float* src = (lane < 16 ? p.k_scales : p.v_scales) + uint64_t(uint32_t(bid)) * p.num_kv_heads +
+                                 hg * p.heads_per_item + l;
+              cp_async4(scales + stage * (2 * kMaxItemHeads) + (lane < 16 ? 0 : kMaxItemHeads) + l, src);
+            }
+            cp_async_arrive(&full[stage]);
+          }
+        }
         if (++stage == p.stages) { stage = 0; phase ^= 1; }
       }
     };
@@ -400,8 +450,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           const uint32_t split = uint32_t(k - a / C);
           // the piece that ends the pair records how many pieces it has
           if (e == b && lane == 0) p.ws_count[uint64_t(s) * p.num_head_groups + hg] = split + 1;
-          emit(s, hg, split, span, span.t0 + int32_t(g - a), span.t0 + int32_t(e - a),
-               (g == a && e == b) ? kSingle : 0);
+          emit(s, hg, split, span, int32_t(g - a), int32_t(e - a), (g == a && e == b) ? kSingle : 0);
           g = e;
         }
         if (nchunks <= gridDim.x) break;
@@ -413,7 +462,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       for (uint64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
         const uint32_t s = uint32_t(it / p.num_head_groups), hg = uint32_t(it % p.num_head_groups);
         const SeqSpan span = seq_span(__ldg(p.seq_lens + s), p);
-        emit(s, hg, 0, span, span.t0, span.t0 + span.ntiles, kSingle);
+        emit(s, hg, 0, span, 0, span.ntiles, kSingle);
       }
     }
     // sentinel: no more work
@@ -425,6 +474,10 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       } else {
         ok = false;
       }
+    }
+    if constexpr (kBlk) {
+      const bool all = __all_sync(0xffffffffu, ok);
+      if (all) mbar_arrive(&full[stage]);
     }
     if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(&g_decode_error, kErrWaitTimeout);
     // No copy may land in shared memory after the CTA exits: wait (bounded,
@@ -463,6 +516,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
 
   float acc[D / 16][4];
   float m_run[2], l_run[2];
+  float mv_run[2];  // kBlk: the running maximum of score + exponent of the V scale
   uint32_t qf[D / 16][2];
   float head_scale[2];
 
@@ -485,6 +539,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
       m_run[0] = m_run[1] = -INFINITY;
+      mv_run[0] = mv_run[1] = -INFINITY;
       l_run[0] = l_run[1] = 0.0f;
       if (!(mt.flags & kEmpty)) {
         const uint16_t* qs = reinterpret_cast<const uint16_t*>(st + p.k_bytes + p.v_bytes) +
@@ -519,7 +574,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           if (amax > 0.0f && amax < INFINITY) {
             int ex;
             frexpf(amax, &ex);
-            e = 15 - ex;
+            e = 15 - ex < 126 ? 15 - ex : 126;  // 2^e and 2^-e stay normal for subnormal rows
           }
           const float sc = ldexpf(1.0f, e);
 #pragma unroll
@@ -570,17 +625,29 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       s[1] += s2[1];
       s[2] += s2[2];
       s[3] += s2[3];
-      s[0] *= head_scale[0];
-      s[1] *= head_scale[1];
-      s[2] *= head_scale[0];
-      s[3] *= head_scale[1];
-      // ---- mask positions outside [start, len)
+      float hs0 = head_scale[0], hs1 = head_scale[1];
+      [[maybe_unused]] float v_exp = 0.0f, v_man = 1.0f;  // kBlk: vs = 2^v_exp v_man
+      if constexpr (kBlk) {
+        const float* sc = scales + stage * (2 * kMaxItemHeads) + hl;
+        const float ks = sc[0];
+        const uint32_t vs = __float_as_uint(sc[kMaxItemHeads]);
+        hs0 *= ks;
+        hs1 *= ks;
+        v_exp = float(int32_t((vs >> 23) & 255u) - 127);
+        v_man = __uint_as_float((vs & 0x007fffffu) | 0x3f800000u);
+      }
+      s[0] *= hs0;
+      s[1] *= hs1;
+      s[2] *= hs0;
+      s[3] *= hs1;
+      // ---- mask positions outside [start, len) and the sinks
       const int32_t p0 = mt.tile * kTile;
-      const bool boundary = p0 < mt.start || p0 + kTile > mt.len;
+      const bool boundary = (p0 < mt.start && p0 + kTile > p.num_sinks) || p0 + kTile > mt.len;
+      auto attended = [&](int32_t pos) { return (pos >= mt.start || pos < p.num_sinks) && pos < mt.len; };
       if (boundary) {
         const int32_t pa = p0 + int32_t(g8), pb = pa + 8;
-        if (pa < mt.start || pa >= mt.len) s[0] = s[1] = -INFINITY;
-        if (pb < mt.start || pb >= mt.len) s[2] = s[3] = -INFINITY;
+        if (!attended(pa)) s[0] = s[1] = -INFINITY;
+        if (!attended(pb)) s[2] = s[3] = -INFINITY;
       }
       // ---- online softmax (base 2), per query head column
       float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
@@ -592,10 +659,21 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
       // Rescale only when some column's running max moved (rare after the
       // first tiles); with the max unchanged the factor would be exactly 1.
-      if (__any_sync(0xffffffffu, mn0 != m_run[0] || mn1 != m_run[1])) {
-        const float al0 = fast_exp2(m_run[0] - mn0), al1 = fast_exp2(m_run[1] - mn1);
+      [[maybe_unused]] float mv0 = 0.0f, mv1 = 0.0f;
+      bool moved = mn0 != m_run[0] || mn1 != m_run[1];
+      if constexpr (kBlk) {
+        mv0 = fmaxf(mv_run[0], mx0 + v_exp);
+        mv1 = fmaxf(mv_run[1], mx1 + v_exp);
+        moved = moved || mv0 != mv_run[0] || mv1 != mv_run[1];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        float al0 = fast_exp2(m_run[0] - mn0), al1 = fast_exp2(m_run[1] - mn1);
         l_run[0] *= al0;
         l_run[1] *= al1;
+        if constexpr (kBlk) {
+          al0 = fast_exp2(mv_run[0] - mv0);
+          al1 = fast_exp2(mv_run[1] - mv1);
+        }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           acc[i][0] *= al0;
@@ -606,6 +684,10 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       }
       m_run[0] = mn0;
       m_run[1] = mn1;
+      if constexpr (kBlk) {
+        mv_run[0] = mv0;
+        mv_run[1] = mv1;
+      }
       const float e0 = fast_exp2(s[0] - mn0), e1 = fast_exp2(s[1] - mn1);
       const float e2 = fast_exp2(s[2] - mn0), e3 = fast_exp2(s[3] - mn1);
       l_run[0] += e0 + e2;
@@ -614,9 +696,8 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       uint32_t vmask01 = 0xffffffffu, vmask89 = 0xffffffffu;
       if (boundary) {
         const int32_t q0 = p0 + 2 * int32_t(c4);
-        auto ok = [&](int32_t pos) { return pos >= mt.start && pos < mt.len; };
-        vmask01 = (ok(q0) ? 0x0000ffffu : 0u) | (ok(q0 + 1) ? 0xffff0000u : 0u);
-        vmask89 = (ok(q0 + 8) ? 0x0000ffffu : 0u) | (ok(q0 + 9) ? 0xffff0000u : 0u);
+        vmask01 = (attended(q0) ? 0x0000ffffu : 0u) | (attended(q0 + 1) ? 0xffff0000u : 0u);
+        vmask89 = (attended(q0 + 8) ? 0x0000ffffu : 0u) | (attended(q0 + 9) ? 0xffff0000u : 0u);
       }
       uint32_t bh0, bh1, bl0, bl1;
       if constexpr (!kFp8V) {
@@ -627,8 +708,18 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         bh0 = movmatrix_trans(hi01), bh1 = movmatrix_trans(hi23);
         bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
       } else {
-        // ---- P^T as f16 hi + lo parts of 2^8 * P
-        const float f0 = e0 * 256.0f, f1 = e1 * 256.0f, f2 = e2 * 256.0f, f3 = e3 * 256.0f;
+        // ---- P^T as f16 hi + lo parts of 2^8 * P (kBlk: of 2^8 * P * vs in
+        // units of 2^M', at most 2^9)
+        float f0, f1, f2, f3;
+        if constexpr (kBlk) {
+          const float c = 256.0f * v_man, o0 = v_exp - mv0, o1 = v_exp - mv1;
+          f0 = fast_exp2(s[0] + o0) * c;
+          f1 = fast_exp2(s[1] + o1) * c;
+          f2 = fast_exp2(s[2] + o0) * c;
+          f3 = fast_exp2(s[3] + o1) * c;
+        } else {
+          f0 = e0 * 256.0f, f1 = e1 * 256.0f, f2 = e2 * 256.0f, f3 = e3 * 256.0f;
+        }
         const uint32_t hi01 = f32x2_to_f16x2(f0, f1), hi23 = f32x2_to_f16x2(f2, f3);
         const uint32_t lo01 = f32x2_to_f16x2(f0 - f16_lo_to_f32(hi01), f1 - f16_hi_to_f32(hi01));
         const uint32_t lo23 = f32x2_to_f16x2(f2 - f16_lo_to_f32(hi23), f3 - f16_hi_to_f32(hi23));
@@ -656,10 +747,14 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       const uint32_t col0 = qt * 8 + 2 * c4;  // query head within the group of column 0
       const uint32_t hq0 = kv_head * p.group + col0;
       const bool ok0 = col0 < p.group, ok1 = col0 + 1 < p.group;
+      float sc0 = kFp8V ? p.out_scale : 1.0f, sc1 = sc0;
+      if constexpr (kBlk) {
+        sc0 *= fast_exp2(mv_run[0] - m_run[0]);
+        sc1 *= fast_exp2(mv_run[1] - m_run[1]);
+      }
       if (mt.flags & kSingle) {
-        const float sc = kFp8V ? p.out_scale : 1.0f;
-        const float inv0 = (mt.flags & kEmpty) ? 0.0f : sc / l0;
-        const float inv1 = (mt.flags & kEmpty) ? 0.0f : sc / l1;
+        const float inv0 = (mt.flags & kEmpty) ? 0.0f : sc0 / l0;
+        const float inv1 = (mt.flags & kEmpty) ? 0.0f : sc1 / l1;
         float* o0 = p.output + (uint64_t(mt.seq) * p.num_q_heads + hq0) * D;
         float* o1 = o0 + D;
 #pragma unroll
@@ -689,9 +784,8 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         for (int i = 0; i < D / 16; ++i) {
           if constexpr (kFp8V) {
             const uint32_t d = i * 16 + 2 * g8;
-            const float sc = p.out_scale;
-            if (ok0) *reinterpret_cast<float2*>(o0 + d) = make_float2(acc[i][0] * sc, acc[i][2] * sc);
-            if (ok1) *reinterpret_cast<float2*>(o1 + d) = make_float2(acc[i][1] * sc, acc[i][3] * sc);
+            if (ok0) *reinterpret_cast<float2*>(o0 + d) = make_float2(acc[i][0] * sc0, acc[i][2] * sc0);
+            if (ok1) *reinterpret_cast<float2*>(o1 + d) = make_float2(acc[i][1] * sc1, acc[i][3] * sc1);
           } else {
             const uint32_t d = i * 16 + g8;
             if (ok0) {
@@ -849,13 +943,13 @@ Geometry geometry(bool fp8, bool fp8_v, uint32_t head_dim, uint32_t num_kv_heads
   return g;
 }
 
-template <bool kFp8, bool kFp8V, int D, int NT>
+template <bool kFp8, bool kFp8V, bool kBlk, int D, int NT>
 int launch_decode_t(const DecodeArgs& a, cudaStream_t stream, const Geometry& geo, DecodeParams& p) {
   CUtensorMap mk, mv;
   if (!encode_pool_map(&mk, a.k_cache, kFp8, a.num_kv_heads, D, geo.heads_per_item) ||
       !encode_pool_map(&mv, a.v_cache, kFp8V, a.num_kv_heads, D, geo.heads_per_item))
     return KV_ERR_CUDA;
-  auto kern = decode_kernel<kFp8, kFp8V, D, NT>;
+  auto kern = decode_kernel<kFp8, kFp8V, kBlk, D, NT>;
   // The dynamic shared-memory opt-in is set once per device and size (so
   // that calls made while a stream is being captured into a CUDA graph after
   // a first eager call issue no attribute change).
@@ -944,6 +1038,9 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.num_head_groups = (a.num_kv_heads + geo.heads_per_item - 1) / geo.heads_per_item;
   p.q_stride = a.q_stride;
   p.sliding_window = a.sliding_window;
+  p.num_sinks = a.num_sinks > uint32_t(INT32_MAX) ? INT32_MAX : int32_t(a.num_sinks);
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
   p.score_scale = a.inv_sqrt_d * kLog2e * (a.fp8 ? a.k_scale : 1.0f);
   p.out_scale = fp8_v ? a.v_scale * (1.0f / 256.0f) : 1.0f;
   p.stages = geo.stages;
@@ -981,26 +1078,32 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     }
   }
 
-  const int key = (fp8_v ? 200 : a.fp8 ? 100 : 0) + int(a.head_dim / 64) * 10 + int(geo.nt);
+  const int key = (a.k_scales ? 300 : fp8_v ? 200 : a.fp8 ? 100 : 0) + int(a.head_dim / 64) * 10 + int(geo.nt);
   switch (key) {
-    case 11: return launch_decode_t<false, false, 64, 1>(a, stream, geo, p);
-    case 12: return launch_decode_t<false, false, 64, 2>(a, stream, geo, p);
-    case 21: return launch_decode_t<false, false, 128, 1>(a, stream, geo, p);
-    case 22: return launch_decode_t<false, false, 128, 2>(a, stream, geo, p);
-    case 41: return launch_decode_t<false, false, 256, 1>(a, stream, geo, p);
-    case 42: return launch_decode_t<false, false, 256, 2>(a, stream, geo, p);
-    case 111: return launch_decode_t<true, false, 64, 1>(a, stream, geo, p);
-    case 112: return launch_decode_t<true, false, 64, 2>(a, stream, geo, p);
-    case 121: return launch_decode_t<true, false, 128, 1>(a, stream, geo, p);
-    case 122: return launch_decode_t<true, false, 128, 2>(a, stream, geo, p);
-    case 141: return launch_decode_t<true, false, 256, 1>(a, stream, geo, p);
-    case 142: return launch_decode_t<true, false, 256, 2>(a, stream, geo, p);
-    case 211: return launch_decode_t<true, true, 64, 1>(a, stream, geo, p);
-    case 212: return launch_decode_t<true, true, 64, 2>(a, stream, geo, p);
-    case 221: return launch_decode_t<true, true, 128, 1>(a, stream, geo, p);
-    case 222: return launch_decode_t<true, true, 128, 2>(a, stream, geo, p);
-    case 241: return launch_decode_t<true, true, 256, 1>(a, stream, geo, p);
-    case 242: return launch_decode_t<true, true, 256, 2>(a, stream, geo, p);
+    case 11: return launch_decode_t<false, false, false, 64, 1>(a, stream, geo, p);
+    case 12: return launch_decode_t<false, false, false, 64, 2>(a, stream, geo, p);
+    case 21: return launch_decode_t<false, false, false, 128, 1>(a, stream, geo, p);
+    case 22: return launch_decode_t<false, false, false, 128, 2>(a, stream, geo, p);
+    case 41: return launch_decode_t<false, false, false, 256, 1>(a, stream, geo, p);
+    case 42: return launch_decode_t<false, false, false, 256, 2>(a, stream, geo, p);
+    case 111: return launch_decode_t<true, false, false, 64, 1>(a, stream, geo, p);
+    case 112: return launch_decode_t<true, false, false, 64, 2>(a, stream, geo, p);
+    case 121: return launch_decode_t<true, false, false, 128, 1>(a, stream, geo, p);
+    case 122: return launch_decode_t<true, false, false, 128, 2>(a, stream, geo, p);
+    case 141: return launch_decode_t<true, false, false, 256, 1>(a, stream, geo, p);
+    case 142: return launch_decode_t<true, false, false, 256, 2>(a, stream, geo, p);
+    case 211: return launch_decode_t<true, true, false, 64, 1>(a, stream, geo, p);
+    case 212: return launch_decode_t<true, true, false, 64, 2>(a, stream, geo, p);
+    case 221: return launch_decode_t<true, true, false, 128, 1>(a, stream, geo, p);
+    case 222: return launch_decode_t<true, true, false, 128, 2>(a, stream, geo, p);
+    case 241: return launch_decode_t<true, true, false, 256, 1>(a, stream, geo, p);
+    case 242: return launch_decode_t<true, true, false, 256, 2>(a, stream, geo, p);
+    case 311: return launch_decode_t<true, true, true, 64, 1>(a, stream, geo, p);
+    case 312: return launch_decode_t<true, true, true, 64, 2>(a, stream, geo, p);
+    case 321: return launch_decode_t<true, true, true, 128, 1>(a, stream, geo, p);
+    case 322: return launch_decode_t<true, true, true, 128, 2>(a, stream, geo, p);
+    case 341: return launch_decode_t<true, true, true, 256, 1>(a, stream, geo, p);
+    case 342: return launch_decode_t<true, true, true, 256, 2>(a, stream, geo, p);
     default: return KV_ERR_UNSUPPORTED;
   }
 }

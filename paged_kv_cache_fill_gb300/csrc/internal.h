@@ -35,6 +35,40 @@ cudaError_t launch_write_fp8(const uint16_t* key, const uint16_t* value, uint8_t
                              uint32_t key_stride, uint32_t value_stride, float k_scale, float v_scale,
                              cudaStream_t stream);
 
+// FP8 K and V write with one scale per (block, KV head); returns a KV_* status.
+struct BlockWriteArgs {
+  const uint16_t* key;
+  const uint16_t* value;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  uint32_t max_blocks_per_seq, num_seqs, num_tokens, num_kv_heads, head_dim, block_size, key_stride, value_stride;
+};
+int launch_write_fp8_block(const BlockWriteArgs& a, cudaStream_t stream);
+cudaError_t read_and_clear_block_write_error(uint32_t* bits);
+
+// Page moves (pages.cu).
+int launch_copy_blocks(void* const* pools, const size_t* block_bytes, uint32_t num_pools, const int32_t* src,
+                       const int32_t* dst, uint32_t num_pairs, uint32_t num_blocks, cudaStream_t stream);
+// first/end null: the entries that a window with sinks has left behind.
+cudaError_t launch_free_blocks(int32_t* tables, int32_t* refs, const int32_t* first, const int32_t* end,
+                               const int32_t* seq_lens, uint32_t max_blocks_per_seq, uint32_t num_seqs,
+                               uint32_t num_blocks, uint32_t block_size, uint32_t sliding_window, uint32_t num_sinks,
+                               cudaStream_t stream);
+int launch_fork_blocks(int32_t* tables, int32_t* seq_lens, int32_t* refs, const int32_t* src_seqs,
+                       const int32_t* dst_seqs, int32_t* copy_src, int32_t* copy_dst, uint32_t num_forks,
+                       uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks, uint32_t block_size,
+                       cudaStream_t stream);
+cudaError_t launch_compact_blocks(const int32_t* tables, const int32_t* refs, int32_t* new_tables, int32_t* new_refs,
+                                  int32_t* new_ids, int32_t* copy_src, int32_t* copy_dst, int32_t* num_used,
+                                  uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks,
+                                  cudaStream_t stream);
+cudaError_t read_and_clear_pages_error(uint32_t* bits);
+
 // Fused RMSNorm/RoPE K write. pos_h/pos_w non-null selects the MRoPE
 // variant (position of pair i from positions/pos_h/pos_w by i % 3); fp8_out
 // stores E4M3(o * inv_scale) into a uint8 pool instead of BF16(o).
@@ -58,7 +92,7 @@ struct PrefillArgs {
   const uint16_t* q;
   const void* k_cache;  // bf16 or e4m3 pool
   const void* v_cache;  // bf16 or (fp8_v) e4m3 pool
-  float* output;
+  void* output;         // float, or bf16 with bf16_out
   const int32_t* block_tables;
   const int32_t* seq_lens;
   const int32_t* query_start_loc;
@@ -66,6 +100,10 @@ struct PrefillArgs {
   float inv_sqrt_d, k_scale, v_scale;
   uint32_t q_stride, sliding_window;
   bool fp8, fp8_v;  // fp8_v implies fp8
+  uint32_t num_sinks;      // first positions that stay visible under a window
+  const float* k_scales;   // non-null (with fp8_v): one scale per (block, KV head) in
+  const float* v_scales;   // place of k_scale and v_scale
+  bool bf16_out;           // the output rows are BF16
 };
 int launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t read_and_clear_prefill_error(uint32_t* bits);
@@ -84,6 +122,9 @@ struct DecodeArgs {
   bool fp8;
   bool fp8_v;     // V is E4M3 too (requires fp8), dequantised by v_scale
   float v_scale;
+  uint32_t num_sinks;     // first positions that stay visible under a window
+  const float* k_scales;  // non-null (with fp8_v): one scale per (block, KV head) in
+  const float* v_scales;  // place of k_scale and v_scale
   void* workspace;
   size_t workspace_bytes;
   bool workspace_fresh;  // registered since the last decode: its counters must be zeroed first
@@ -107,10 +148,12 @@ cudaError_t debug_set_pool_kv_write(uint32_t num_blocks, uint32_t block_size);
 cudaError_t debug_set_pool_fused_k(uint32_t num_blocks, uint32_t block_size);
 cudaError_t debug_set_pool_decode(uint32_t num_blocks, uint32_t block_size);
 cudaError_t debug_set_pool_prefill(uint32_t num_blocks, uint32_t block_size);
+cudaError_t debug_set_pool_block_write(uint32_t num_blocks, uint32_t block_size);
 cudaError_t debug_read_and_clear_kv_write(uint32_t* bits);
 cudaError_t debug_read_and_clear_fused_k(uint32_t* bits);
 cudaError_t debug_read_and_clear_decode(uint32_t* bits);
 cudaError_t debug_read_and_clear_prefill(uint32_t* bits);
+cudaError_t debug_read_and_clear_block_write(uint32_t* bits);
 cudaError_t debug_set_wait_limit_decode(uint64_t ns);
 #endif
 

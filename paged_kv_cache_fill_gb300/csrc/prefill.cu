@@ -1,5 +1,7 @@
 // Multi-token (chunked-prefill) paged attention over a BF16, an FP8-E4M3-K /
-// BF16-V or an FP8-E4M3 K and V paged cache.
+// BF16-V or an FP8-E4M3 K and V paged cache, the last with scalar scales or
+// with one scale for each block and KV head; causal, with a sliding window and
+// first positions that stay visible under it (sinks) where asked for.
 //
 // [kv_cache.rs] "Batched prefill variants (N tokens)" (a heading only), read
 // as: sequence s brings n_s = query_start_loc[s+1] - query_start_loc[s]
@@ -40,17 +42,21 @@ struct PrefillParams {
   const int32_t* block_tables;
   const int32_t* seq_lens;
   const int32_t* qsl;  // query_start_loc
-  float* output;
+  void* output;        // float rows, or BF16 ones (bf16_out)
   uint32_t max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, group;
   uint32_t block_size, block_shift, q_stride, sliding_window;
+  int32_t num_sinks;      // first positions that stay visible under a window
+  uint32_t bf16_out;
+  const float* k_scales;  // kBlk: [num_blocks, num_kv_heads]
+  const float* v_scales;
   float score_scale;  // inv_sqrt_d * log2(e) (times k_scale for FP8)
   float out_scale;    // E4M3 V: v_scale (the V codes enter the PV product as they are)
 };
 
 // An E4M3 tile [chunk of 128 dims][128 keys][128 B] (head_dim 64: [128
 // keys][64 B], 64-byte swizzled) -> the f16 tile [chunk of 64 dims][128
-// keys][128 B], 128-byte swizzled; rows at or past `live`
-// become zeros. Exact (every E4M3 value is an f16 value). Lane l takes keys
+// keys][128 B], 128-byte swizzled; rows at or past `live` and rows [dead0,
+// dead1) become zeros. Exact (every E4M3 value is an f16 value). Lane l takes keys
 // l, l + 32 (first pass) and l + 64, l + 96 (second). Each pass loads its
 // two rows (16 x 16 B) before any store: the stores could alias the loads as
 // far as the compiler knows, so interleaving them would serialise every
@@ -62,7 +68,7 @@ struct PrefillParams {
 // instruction fetch).
 template <int D>
 __device__ __noinline__ void e4m3_tile_to_f16(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst,
-                                              int32_t live, uint32_t lane) {
+                                              int32_t live, int32_t dead0, int32_t dead1, uint32_t lane) {
   constexpr uint32_t kUnits = D < 128 ? D / 16 : 8;  // 16-byte units of a source row per chunk
   constexpr uint32_t kSrcChunks = (D + 127) / 128;
   // unit u of key r in source chunk c8
@@ -78,7 +84,7 @@ __device__ __noinline__ void e4m3_tile_to_f16(const uint8_t* __restrict__ src, u
 #pragma unroll
       for (uint32_t k = 0; k < 2; ++k) {
         const uint32_t r = r0 + 32 * k + lane;
-        const bool keep = int32_t(r) < live;
+        const bool keep = int32_t(r) < live && (int32_t(r) < dead0 || int32_t(r) >= dead1);
 #pragma unroll
         for (uint32_t u = 0; u < kUnits; ++u) {
           w[k][u] = *src_unit(c8, r, u);
@@ -134,6 +140,14 @@ __device__ __forceinline__ uint32_t len_class(uint64_t tiles) {
   return c < kLenClasses ? c : kLenClasses - 1;
 }
 
+// Tiles of the sinks below a window that begins at key k_lo: those before the
+// window's first tile (which covers the sinks that lie in it).
+__device__ __forceinline__ int64_t sink_tiles(int32_t num_sinks, int64_t k_lo) {
+  const int64_t s = num_sinks < k_lo ? num_sinks : k_lo;
+  const int64_t t = (s + kTcBN - 1) / kTcBN;
+  return t < k_lo / kTcBN ? t : k_lo / kTcBN;
+}
+
 // Sequence s's share of the item list: its query tokens n, its items (row
 // blocks x KV heads) and the length class of its queries' key range.
 // A bad query layout counts as no queries (flagged once, by the caller's
@@ -155,7 +169,7 @@ __device__ __forceinline__ uint32_t seq_items(const PrefillParams& p, uint32_t s
   L = L < 0 ? 0 : (L > cap ? cap : L);
   int64_t k_lo = 0;
   if (p.sliding_window > 0 && L - n + 1 - int64_t(p.sliding_window) > 0) k_lo = L - n + 1 - p.sliding_window;
-  const int64_t tiles = (L + kTcBN - 1) / kTcBN - k_lo / kTcBN;
+  const int64_t tiles = (L + kTcBN - 1) / kTcBN - k_lo / kTcBN + sink_tiles(p.num_sinks, k_lo);
   cls = len_class(tiles > 0 ? uint64_t(tiles) : 0);
   return row_blocks<BM>(n, p.group) * p.num_kv_heads;
 }
@@ -294,6 +308,21 @@ constexpr float kRescaleLog2 = 8.0f;  // reference-max slack of the online softm
 //     then free Q tiles and K/V stages and stores it with one bulk copy
 //     (direct stores of a row per thread wrote 16 bytes per 32-byte sector
 //     and took ~3 us per CTA).
+// Block scales (kBlk). A group of 16 keys (one TMA box) lies in one cache
+// block, so it has one K scale ks and one V scale vs. The K producer's lanes 0
+// to 7 load them a tile ahead (lane g those of group g) and put ks, log2 vs and
+// 1 / vs into a ring of kScaleSlots tiles. With z = x rs ks the score, the
+// weight that enters the PV product is P' = 2^(z + log2 vs - M'), M' the
+// running maximum of z + log2 vs: the codes' products need no further scale,
+// the f16 weights keep their precision whatever the scales are, and one
+// exponential per score is enough, since the softmax sum is
+// l = sum over groups of (sum of the group's P') / vs, in the same frame.
+// A slot is rewritten kScaleSlots tiles later: when the K producer has the K
+// stage of tile i, the softmax of tile i - 5 is done in both Q tiles (their S
+// products of tile i - 4 have run, and each follows that tile's P).
+constexpr uint32_t kScaleSlots = 8;
+constexpr uint32_t kGroups = kTcBN / kSub;  // groups of keys with one scale, per tile
+
 constexpr int kTc2Rows = 256;
 // registers per thread of warpgroup 0 and of the softmax warpgroups after
 // setmaxnreg (per variant, the split that ptxas fits without spills or the
@@ -332,11 +361,12 @@ struct Tc2Layout {  // byte offsets from the 1024-aligned shared base
   static __device__ __forceinline__ constexpr uint32_t o_col(uint32_t t) { return 128u + (t << 8); }
 };
 
-template <int D, bool kFp8, bool kFp8V>
+template <int D, bool kFp8, bool kFp8V, bool kBlk>
 __global__ void __launch_bounds__(32 * 12, 1)
     prefill_tc2_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const PrefillParams p) {
   static_assert(kFp8 || !kFp8V, "an E4M3 V cache comes with an E4M3 K cache");
+  static_assert(kFp8V || !kBlk, "block scales come with an E4M3 K and V cache");
   using Lay = Tc2Layout<D, kFp8, kFp8V>;
   constexpr uint32_t kChunks = Lay::kChunks;
   extern __shared__ uint8_t smem_raw[];
@@ -348,6 +378,9 @@ __global__ void __launch_bounds__(32 * 12, 1)
   __shared__ uint64_t v8_full[kTcStages];                        // E4M3 V: loaded
   __shared__ uint64_t s_full[2], p_full[2], o_full[2];  // per Q tile
   __shared__ uint64_t q_full, mma_done;
+  __shared__ uint64_t sc_full[kBlk ? kScaleSlots : 1];  // kBlk: a tile's scales are in their slot
+  __shared__ __align__(16) float sc_k[kBlk ? kScaleSlots : 1][kGroups], sc_v[kBlk ? kScaleSlots : 1][kGroups],
+      sc_vinv[kBlk ? kScaleSlots : 1][kGroups];  // ks, log2 vs, 1 / vs
   __shared__ uint32_t tmem_base_s;
   __shared__ Item s_item;
 
@@ -369,6 +402,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
       mbar_init(&p_full[t], kTcBM);
       mbar_init(&o_full[t], 1);
     }
+    if constexpr (kBlk)
+      for (uint32_t s = 0; s < kScaleSlots; ++s) mbar_init(&sc_full[s], kGroups);
     mbar_init(&q_full, 2 * kTcBM);
     mbar_init(&mma_done, 1);
     fence_mbar_init();
@@ -396,7 +431,12 @@ __global__ void __launch_bounds__(32 * 12, 1)
   if (W > 0 && pos_first + 1 - W > 0) k_lo = pos_first + 1 - W;
   const int32_t t_begin = k_lo / kTcBN;
   const int32_t t_end = k_hi > 0 ? (k_hi + kTcBN - 1) / kTcBN : t_begin;
-  const int32_t T = t_end - t_begin;
+  // the item's key tiles: the sinks' ones, then those from the window's first;
+  // no row of the item attends the keys [dead_lo, k_lo)
+  const int32_t nsk = int32_t(sink_tiles(p.num_sinks, k_lo));
+  const int32_t T = t_end - t_begin + nsk;
+  const int32_t dead_lo = p.num_sinks < k_lo ? p.num_sinks : k_lo;
+  auto key_base_of = [&](int32_t i) { return (i < nsk ? i : t_begin + i - nsk) * kTcBN; };
 
   if (warp < 4) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(tc2_regs_low<kFp8V>()));
@@ -411,15 +451,16 @@ __global__ void __launch_bounds__(32 * 12, 1)
     const uint32_t chunks = e4m3 ? Lay::kK8Chunks : kChunks;
     const uint32_t row_bytes = e4m3 ? Lay::kE4Row : 128u;  // of a key's row per box
     // E4M3 V tile j -> its f16 stage (in place at head_dim 128, from its own
-    // ring at head_dim 64); rows at or past the item's last key (not
-    // loaded, or positions past every query) become zeros
+    // ring at head_dim 64); rows at or past the item's last key and rows
+    // that no query of the item attends (not loaded, or holding anything)
+    // become zeros
     auto convert_v = [&](int32_t j) -> bool {
       const uint32_t sj = uint32_t(j) % kTcStages;
       if (!__all_sync(0xffffffffu, mbar_wait(&v8_full[sj], uint32_t(j / kTcStages) & 1))) return false;
       uint8_t* vt = smem + Lay::kStage0 + sj * Lay::kStageBytes + Lay::kKBytes;  // [chunk][128 keys][128 B]
-      const int32_t live = k_hi - (t_begin + j) * kTcBN;
+      const int32_t kb = key_base_of(j), live = k_hi - kb, dead0 = dead_lo - kb, dead1 = k_lo - kb;
       if constexpr (Lay::kV8Ring) {
-        e4m3_tile_to_f16<D>(smem + Lay::kV80 + sj * Lay::kV8Bytes, vt, live, lane);
+        e4m3_tile_to_f16<D>(smem + Lay::kV80 + sj * Lay::kV8Bytes, vt, live, dead0, dead1, lane);
       } else {
 #pragma unroll 1
         for (uint32_t r = lane; r < uint32_t(kTcBN); r += 32) {
@@ -427,7 +468,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
           uint4 w[8];
 #pragma unroll
           for (uint32_t u = 0; u < 8; ++u) w[u] = *reinterpret_cast<const uint4*>(row1 + ((u ^ (r & 7)) << 4));
-          if (int32_t(r) >= live) {
+          if (int32_t(r) >= live || (int32_t(r) >= dead0 && int32_t(r) < dead1)) {
 #pragma unroll
             for (uint32_t u = 0; u < 8; ++u) w[u] = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -455,13 +496,38 @@ __global__ void __launch_bounds__(32 * 12, 1)
     const int32_t* table = p.block_tables + uint64_t(it.seq) * p.max_blocks_per_seq;
     bool ok = true;
     int32_t issued = 0;
+    // the box of tile i that this lane loads: 16 keys, unless no row of the
+    // item attends any of them (whose page may be gone)
+    auto my_box = [&](int32_t i, int32_t& key0) -> bool {
+      key0 = key_base_of(i) + int32_t(lane) * kSub;
+      return lane < uint32_t(kTcBN / kSub) && key0 < k_hi && !(key0 >= dead_lo && key0 + kSub <= k_lo);
+    };
+    // kBlk: this lane's group's scales, loaded a tile ahead (1 where no box is
+    // loaded). A negative block id (outside the caller's contract; its box is
+    // filled with zeros) takes block 0's.
+    [[maybe_unused]] float ks_next = 1.0f, vs_next = 1.0f;
+    auto load_scales = [&](int32_t i) {
+      int32_t key0;
+      ks_next = vs_next = 1.0f;
+      if (i < T && my_box(i, key0)) {
+        int32_t bid = __ldg(table + (key0 >> p.block_shift));
+#ifdef PAGEDKV_DEBUG_BOUNDS
+        bid = dbg_block_ok(bid) ? bid : 0;
+#endif
+        const uint64_t at = uint64_t(uint32_t(bid > 0 ? bid : 0)) * p.num_kv_heads + uint32_t(it.kv_head);
+        ks_next = __ldg(p.k_scales + at);
+        vs_next = __ldg(p.v_scales + at);
+      }
+    };
+    if constexpr (kBlk)
+      if (is_k) load_scales(0);
     for (int32_t i = 0; i < T && ok; ++i) {
       // E4M3 V: the tile before this one is converted as soon as it has
       // landed, before this tile's stage is waited for (PV two tiles back)
       if (self_converts && i >= 1 && !(ok = convert_v(i - 1))) break;
       const uint32_t st = uint32_t(i) % kTcStages;
-      const int32_t key0 = (t_begin + i) * kTcBN + int32_t(lane) * kSub;
-      const bool mine = lane < uint32_t(kTcBN / kSub) && key0 < k_hi;
+      int32_t key0;
+      const bool mine = my_box(i, key0);
       const int32_t block_id = mine ? __ldg(table + (key0 >> p.block_shift)) : 0;
       // stage st was last filled for tile i - 2: free once its last reader is done
       if (lane == 0 && i >= kTcStages && !mbar_wait(&empty[st], uint32_t((i - kTcStages) / kTcStages) & 1))
@@ -489,6 +555,21 @@ __global__ void __launch_bounds__(32 * 12, 1)
         for (uint32_t c = 0; c < chunks; ++c)
           tma_load_3d(dst + c * (kTcBN * row_bytes), map, 0, slot0, it.kv_head * chunks + c, &full[st]);
       }
+      if constexpr (kBlk) {
+        if (is_k) {
+          if (lane < kGroups) {
+            const uint32_t sl = uint32_t(i) % kScaleSlots;
+            const uint32_t vb = __float_as_uint(vs_next);
+            // the exponent, and log2 of the fraction in [1, 2): exact for powers of two
+            const float man = __uint_as_float((vb & 0x007fffffu) | 0x3f800000u);
+            sc_k[sl][lane] = ks_next;
+            sc_v[sl][lane] = float(int32_t((vb >> 23) & 255u) - 127) + (man == 1.0f ? 0.0f : log2f(man));
+            sc_vinv[sl][lane] = 1.0f / vs_next;
+            mbar_arrive(&sc_full[sl]);
+          }
+          load_scales(i + 1);
+        }
+      }
       issued = i + 1;
     }
     if (self_converts && ok && T > 0) ok = convert_v(T - 1);
@@ -511,7 +592,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&v8_full[sj], uint32_t(j / kTcStages) & 1));
       if (!ok) break;
       uint4* units = reinterpret_cast<uint4*>(smem + Lay::kStage0 + sj * Lay::kStageBytes + Lay::kKBytes);
-      const int32_t live = k_hi - (t_begin + j) * kTcBN;
+      const int32_t kb = key_base_of(j), live = k_hi - kb, dead0 = dead_lo - kb, dead1 = k_lo - kb;
 #pragma unroll 1
       for (uint32_t e0 = kHalf; e0 < 2 * kHalf; e0 += 8 * 32) {
         uint4 w[8];
@@ -528,10 +609,12 @@ __global__ void __launch_bounds__(32 * 12, 1)
           }
           w[u] = make_uint4(ws[0], ws[1], ws[2], ws[3]);
         }
-        if (live < kTcBN) {
+        if (live < kTcBN || dead1 > 0) {
 #pragma unroll
-          for (uint32_t u = 0; u < 8; ++u)
-            if (int32_t(((e0 + 32 * u + lane) >> 3) % uint32_t(kTcBN)) >= live) w[u] = make_uint4(0, 0, 0, 0);
+          for (uint32_t u = 0; u < 8; ++u) {
+            const int32_t r = int32_t(((e0 + 32 * u + lane) >> 3) % uint32_t(kTcBN));
+            if (r >= live || (r >= dead0 && r < dead1)) w[u] = make_uint4(0, 0, 0, 0);
+          }
         }
 #pragma unroll
         for (uint32_t u = 0; u < 8; ++u) units[e0 + 32 * u + lane] = w[u];
@@ -687,7 +770,9 @@ __global__ void __launch_bounds__(32 * 12, 1)
     const int32_t grow = it.row0 + r;
     const int32_t tok = grow / g, hh = grow % g;
     const int32_t pos = valid ? it.len - it.n + tok : -1;  // -1: attends nothing
+    // under a window the row skips the keys [num_sinks, pos + 1 - W)
     const int32_t lo = W > 0 ? pos + 1 - W : INT32_MIN;
+    const uint32_t skipped = lo > p.num_sinks ? uint32_t(lo - p.num_sinks) : 0u;
     // the Q row into the tile's shared-memory tile ([chunk][row][128 B],
     // 128-byte swizzled), zeros past the item. E4M3 K cache: the row as f16,
     // times 2^e with e chosen so that its largest magnitude lies in
@@ -715,7 +800,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
         if (amax > 0.0f && amax < INFINITY) {
           int ex;
           frexpf(amax, &ex);
-          e = 15 - ex;
+          e = 15 - ex < 126 ? 15 - ex : 126;  // 2^e and 2^-e stay normal for subnormal rows
         }
         const float sc = ldexpf(1.0f, e);
         rs = p.score_scale * ldexpf(1.0f, -e);
@@ -744,8 +829,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
       // second half: each value times
       // 2^-8, rounded to f16 (exact for 2^-6 <= |v| < 2^24, within 2^-17
       // absolute below; the output scale undoes 2^-8). Rows at or past the
-      // item's last key (not loaded, or positions past every query) become
-      // zeros. Elementwise, so the swizzle does not matter: 16-byte unit e of
+      // item's last key and rows that no query of the item attends (not
+      // loaded, or holding anything) become zeros. Elementwise, so the swizzle does not matter: 16-byte unit e of
       // the tile ([chunk][128 keys][128 B]) holds key row (e / 8) % 128, and
       // a warp's access covers 32 consecutive units.
       auto convert_v_half = [&](int32_t j, uint32_t h) -> bool {
@@ -754,7 +839,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
         const uint32_t sj = uint32_t(j) % kTcStages;
         if (!__all_sync(0xffffffffu, mbar_wait(&v8_full[sj], uint32_t(j / kTcStages) & 1))) return false;
         uint4* units = reinterpret_cast<uint4*>(smem + Lay::kStage0 + sj * Lay::kStageBytes + Lay::kKBytes);
-        const int32_t live = k_hi - (t_begin + j) * kTcBN;
+        const int32_t kb = key_base_of(j), live = k_hi - kb, dead0 = dead_lo - kb, dead1 = k_lo - kb;
         const F2 down = f2_make(0.00390625f, 0.00390625f);
         constexpr uint32_t kPass = kPer < 4 ? kPer : 4;  // units per pass
 #pragma unroll 1
@@ -773,11 +858,12 @@ __global__ void __launch_bounds__(32 * 12, 1)
             }
             w[u] = make_uint4(ws[0], ws[1], ws[2], ws[3]);
           }
-          if (live < kTcBN) {  // the item's last tile
+          if (live < kTcBN || dead1 > 0) {  // the item's last tile, a sink tile or the window's first
 #pragma unroll
-            for (uint32_t u = 0; u < kPass; ++u)
-              if (int32_t(((h * kHalf + (u0 + u) * kTcBM + row) >> 3) % uint32_t(kTcBN)) >= live)
-                w[u] = make_uint4(0, 0, 0, 0);
+            for (uint32_t u = 0; u < kPass; ++u) {
+              const int32_t r = int32_t(((h * kHalf + (u0 + u) * kTcBM + row) >> 3) % uint32_t(kTcBN));
+              if (r >= live || (r >= dead0 && r < dead1)) w[u] = make_uint4(0, 0, 0, 0);
+            }
           }
 #pragma unroll
           for (uint32_t u = 0; u < kPass; ++u) units[h * kHalf + (u0 + u) * kTcBM + row] = w[u];
@@ -809,28 +895,47 @@ __global__ void __launch_bounds__(32 * 12, 1)
         float x[kTcBN];
 #pragma unroll
         for (int k = 0; k < kTcBN; ++k) x[k] = __uint_as_float(sv[k]);
-        const int32_t key_base = (t_begin + j) * kTcBN;
+        const int32_t key_base = key_base_of(j);
         if (key_base + kTcBN - 1 > pos || key_base < lo) {
+          const uint32_t off = uint32_t(key_base - p.num_sinks);
 #pragma unroll
           for (int k = 0; k < kTcBN; ++k)
-            if (key_base + k > pos || key_base + k < lo) x[k] = -INFINITY;
+            if (key_base + k > pos || off + uint32_t(k) < skipped) x[k] = -INFINITY;
         }
-        // the tile max: eight partial maxima, two scores into each per
-        // three-input max
-        float xm8[8];
+        float tile_max;
+        if constexpr (kBlk) {
+          // per group of 16 keys: the largest score times the group's scale,
+          // plus log2 of its V scale
+          ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[uint32_t(j) % kScaleSlots], uint32_t(j / kScaleSlots) & 1));
+          if (!ok) break;
+          const float* ks = sc_k[uint32_t(j) % kScaleSlots];
+          const float* vl = sc_v[uint32_t(j) % kScaleSlots];
+          float gm[kGroups];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) xm8[q] = x[q];
+          for (int g2 = 0; g2 < int(kGroups); ++g2) {
+            const float* xg = x + kSub * g2;
+            const float a = fmax3(fmax3(xg[0], xg[1], xg[2]), xg[3], xg[4]), b = fmax3(fmax3(xg[5], xg[6], xg[7]), xg[8], xg[9]);
+            const float c = fmax3(fmax3(xg[10], xg[11], xg[12]), xg[13], xg[14]);
+            gm[g2] = fmaf(fmax3(fmaxf(a, xg[15]), b, c) * rs, ks[g2], vl[g2]);
+          }
+          tile_max = fmax3(fmax3(gm[0], gm[1], gm[2]), fmax3(gm[3], gm[4], gm[5]), fmaxf(gm[6], gm[7]));
+        } else {
+          // the tile max: eight partial maxima, two scores into each per
+          // three-input max
+          float xm8[8];
 #pragma unroll
-        for (int k = 8; k + 8 < kTcBN; k += 16) {
+          for (int q = 0; q < 8; ++q) xm8[q] = x[q];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) xm8[q] = fmax3(xm8[q], x[k + q], x[k + 8 + q]);
+          for (int k = 8; k + 8 < kTcBN; k += 16) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) xm8[q] = fmax3(xm8[q], x[k + q], x[k + 8 + q]);
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) xm8[q] = fmaxf(xm8[q], x[kTcBN - 8 + q]);
+          tile_max = rs * fmax3(fmax3(xm8[0], xm8[1], xm8[2]), fmax3(xm8[3], xm8[4], xm8[5]), fmaxf(xm8[6], xm8[7]));
         }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) xm8[q] = fmaxf(xm8[q], x[kTcBN - 8 + q]);
-        const float xm = fmax3(fmax3(xm8[0], xm8[1], xm8[2]), fmax3(xm8[3], xm8[4], xm8[5]), fmaxf(xm8[6], xm8[7]));
         // the row's reference max moves only when the tile max exceeds it
         // by more than kRescaleLog2 (or on its first finite score)
-        const float tile_max = xm * rs;
         const float mx = (m_run == -INFINITY || tile_max > m_run + kRescaleLog2) ? fmaxf(m_run, tile_max) : m_run;
         const float mb = mx == -INFINITY ? 0.0f : mx;
         // the weights are formed as 2^7 P (<= 2^15), so that they stay above
@@ -841,26 +946,54 @@ __global__ void __launch_bounds__(32 * 12, 1)
         // each pair of weights goes to f16 as soon as it is formed (|P - P16|
         // <= 2^-11 P above 2^-21 P, the weights being 2^7 P), so that few
         // packed words stay live
-        const F2 sc2 = f2_make(rs, rs), nmb2 = f2_make(-mbp, -mbp);
-        F2 sum2[4] = {0ull, 0ull, 0ull, 0ull};
+        float sum = 0.0f;
         // P over the S columns, keys 2m, 2m + 1 in column m, 32 keys at a
         // time (the V rows of keys at or past k_hi were zeroed as the tile
         // was converted)
+        if constexpr (kBlk) {
+          const float* ks = sc_k[uint32_t(j) % kScaleSlots];
+          const float* vl = sc_v[uint32_t(j) % kScaleSlots];
+          const float* vi = sc_vinv[uint32_t(j) % kScaleSlots];
 #pragma unroll
-        for (int c = 0; c < kTcBN / 32; ++c) {
-          uint32_t pw[16];
+          for (int c = 0; c < kTcBN / 32; ++c) {
+            uint32_t pw[16];
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const int k = 16 * c + q;
-            const float2 a = f2_split(f2_fma(f2_make(x[2 * k], x[2 * k + 1]), sc2, nmb2));
-            const float e0 = fast_exp2(a.x), e1 = fast_exp2(a.y);
-            sum2[q & 3] = f2_add(sum2[q & 3], f2_make(e0, e1));
-            pw[q] = f32x2_to_f16x2(e0, e1);
+            for (int g2 = 0; g2 < 2; ++g2) {
+              const float a = rs * ks[2 * c + g2], b = vl[2 * c + g2] - mbp;
+              const F2 sc2 = f2_make(a, a), add2 = f2_make(b, b);
+              F2 sum2[2] = {0ull, 0ull};
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const int k = 16 * c + 8 * g2 + q;
+                const float2 e = f2_split(f2_fma(f2_make(x[2 * k], x[2 * k + 1]), sc2, add2));
+                const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+                sum2[q & 1] = f2_add(sum2[q & 1], f2_make(e0, e1));
+                pw[8 * g2 + q] = f32x2_to_f16x2(e0, e1);
+              }
+              const float2 s01 = f2_split(f2_add(sum2[0], sum2[1]));
+              sum = fmaf(s01.x + s01.y, vi[2 * c + g2], sum);
+            }
+            tmem_st16(scol + 16 * c, pw);
           }
-          tmem_st16(scol + 16 * c, pw);
+        } else {
+          const F2 sc2 = f2_make(rs, rs), nmb2 = f2_make(-mbp, -mbp);
+          F2 sum2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < kTcBN / 32; ++c) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const int k = 16 * c + q;
+              const float2 a = f2_split(f2_fma(f2_make(x[2 * k], x[2 * k + 1]), sc2, nmb2));
+              const float e0 = fast_exp2(a.x), e1 = fast_exp2(a.y);
+              sum2[q & 3] = f2_add(sum2[q & 3], f2_make(e0, e1));
+              pw[q] = f32x2_to_f16x2(e0, e1);
+            }
+            tmem_st16(scol + 16 * c, pw);
+          }
+          const float2 s01 = f2_split(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])));
+          sum = s01.x + s01.y;
         }
-        const float2 s01 = f2_split(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])));
-        const float sum = s01.x + s01.y;
         const float al = fast_exp2(m_run - mb);
         const bool rescale = j > 0 && __any_sync(0xffffffffu, mx != m_run);
         if (rescale) {
@@ -891,12 +1024,14 @@ __global__ void __launch_bounds__(32 * 12, 1)
       // the PV product summed E4M3 codes (v_scale dequantises them) or BF16
       // values times 2^-8
       const float inv = l_run > 0.0f ? (kFp8V ? p.out_scale : 256.0f) / l_run : 0.0f;
-      float* o = valid ? p.output + (uint64_t(it.qstart + tok) * p.num_q_heads + uint64_t(it.kv_head * g + hh)) * D
-                       : nullptr;
+      const uint32_t out_bytes = p.bf16_out ? D * 2 : D * 4;  // of a row
+      uint8_t* o = valid ? static_cast<uint8_t*>(p.output) +
+                               (uint64_t(it.qstart + tok) * p.num_q_heads + uint64_t(it.kv_head * g + hh)) * out_bytes
+                         : nullptr;
       bool done = __all_sync(0xffffffffu, ok);
       if (T == 0) {  // no key for any query of the item: zeros
         if (o && done)
-          for (uint32_t c = 0; c < uint32_t(D); c += 4) *reinterpret_cast<float4*>(o + c) = make_float4(0, 0, 0, 0);
+          for (uint32_t c = 0; c < out_bytes; c += 16) *reinterpret_cast<float4*>(o + c) = make_float4(0, 0, 0, 0);
       } else if (done) {
         // once every product is done, the Q tiles and the K/V stages are free:
         // the row is staged there (rows D * 4 + 16 bytes apart, so that the
@@ -913,15 +1048,26 @@ __global__ void __launch_bounds__(32 * 12, 1)
           uint32_t ov[32];
           tmem_ld32(ocol + c0, ov);
           tmem_wait_ld();
+          if (p.bf16_out) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(stage + c0 + k) =
-                make_float4(__uint_as_float(ov[k]) * inv, __uint_as_float(ov[k + 1]) * inv,
-                            __uint_as_float(ov[k + 2]) * inv, __uint_as_float(ov[k + 3]) * inv);
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t h[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                h[q] = f32x2_to_bf16x2(__uint_as_float(ov[k + 2 * q]) * inv, __uint_as_float(ov[k + 2 * q + 1]) * inv);
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(stage) + c0 + k) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(stage + c0 + k) =
+                  make_float4(__uint_as_float(ov[k]) * inv, __uint_as_float(ov[k + 1]) * inv,
+                              __uint_as_float(ov[k + 2]) * inv, __uint_as_float(ov[k + 3]) * inv);
+          }
         }
         if (o && done) {
           fence_async_smem();
-          bulk_store(o, stage, D * 4);
+          bulk_store(o, stage, out_bytes);
           bulk_store_wait_read();
         }
       }
@@ -935,7 +1081,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
   }
 }
 
-template <int D, bool kFp8, bool kFp8V>
+template <int D, bool kFp8, bool kFp8V, bool kBlk>
 int launch_prefill_tc2(const PrefillArgs& a, cudaStream_t stream, PrefillParams& p) {
   CUtensorMap mk, mv;
   if (!encode_pool_map(&mk, a.k_cache, kFp8, a.num_kv_heads, D, 1, 1) ||
@@ -950,7 +1096,7 @@ int launch_prefill_tc2(const PrefillArgs& a, cudaStream_t stream, PrefillParams&
   // all 512 TMEM columns: no second CTA may be resident on an SM
   constexpr int kNeed = int(1024 + Tc2Layout<D, kFp8, kFp8V>::kBytes);
   const int smem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
-  auto kern = prefill_tc2_kernel<D, kFp8, kFp8V>;
+  auto kern = prefill_tc2_kernel<D, kFp8, kFp8V, kBlk>;
   static int set_bytes[64] = {0};
   const int dev_id = device_info().device;
   if (dev_id < 0 || dev_id >= 64) return KV_ERR_CUDA;
@@ -982,16 +1128,22 @@ int launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   p.block_shift = uint32_t(__builtin_ctz(a.block_size));
   p.q_stride = a.q_stride;
   p.sliding_window = a.sliding_window;
+  p.num_sinks = a.num_sinks > uint32_t(INT32_MAX) ? INT32_MAX : int32_t(a.num_sinks);
+  p.bf16_out = a.bf16_out;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
   p.score_scale = a.inv_sqrt_d * kLog2e * (a.fp8 ? a.k_scale : 1.0f);
   p.out_scale = a.fp8_v ? a.v_scale : 1.0f;
-  const int key = (a.fp8_v ? 200 : a.fp8 ? 100 : 0) + int(a.head_dim);
+  const int key = (a.k_scales ? 300 : a.fp8_v ? 200 : a.fp8 ? 100 : 0) + int(a.head_dim);
   switch (key) {
-    case 64: return launch_prefill_tc2<64, false, false>(a, stream, p);  // tcgen05 / TMEM, two Q tiles per CTA
-    case 128: return launch_prefill_tc2<128, false, false>(a, stream, p);
-    case 164: return launch_prefill_tc2<64, true, false>(a, stream, p);
-    case 228: return launch_prefill_tc2<128, true, false>(a, stream, p);
-    case 264: return launch_prefill_tc2<64, true, true>(a, stream, p);
-    case 328: return launch_prefill_tc2<128, true, true>(a, stream, p);
+    case 64: return launch_prefill_tc2<64, false, false, false>(a, stream, p);  // tcgen05 / TMEM, two Q tiles per CTA
+    case 128: return launch_prefill_tc2<128, false, false, false>(a, stream, p);
+    case 164: return launch_prefill_tc2<64, true, false, false>(a, stream, p);
+    case 228: return launch_prefill_tc2<128, true, false, false>(a, stream, p);
+    case 264: return launch_prefill_tc2<64, true, true, false>(a, stream, p);
+    case 328: return launch_prefill_tc2<128, true, true, false>(a, stream, p);
+    case 364: return launch_prefill_tc2<64, true, true, true>(a, stream, p);
+    case 428: return launch_prefill_tc2<128, true, true, true>(a, stream, p);
     default: return KV_ERR_UNSUPPORTED;
   }
 }
