@@ -323,9 +323,8 @@ PAGEDKV_API int paged_prefill_attn_fp8(const kv_bf16_t *q, const kv_e4m3_t *k_ca
  * array's device address (cudaGetSymbolAddress) and caches it: make that
  * first call before any stream capture, and do not call it on a device
  * after a cudaDeviceReset in the same process (the cached address belonged
- * to the reset context). All calls share the one array, which keeps the
- * previous call's contents; each call clears the counters that must start
- * at zero on its own stream first. Calls whose work may overlap on the GPU
+ * to the reset context). All calls share the one array; no call reads what
+ * an earlier one left there. Calls whose work may overlap on the GPU
  * (different streams, other devices' calls aside) race on the array: order
  * them.
  * ---------------------------------------------------------------------- */

@@ -144,12 +144,25 @@ def _check(name: str, status: int) -> None:
         raise PagedKVError(name, status)
 
 
+# The smallest calls are bound by this module, not by their kernels, so a tensor
+# that passes costs four short calls into torch; what is wrong with one that
+# does not is found out afterwards (a 9-tensor call: 20 us of host time with a
+# torch.cuda.current_device() per tensor and a Stream object, 10 us like this).
+_device = torch._C._cuda_getDevice
+
+
 def _ptr(t: torch.Tensor | None):
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor")
-    if t.numel():
+    if t.get_device() != _device() or not t.is_contiguous():
+        _refuse(t)
+    return t.data_ptr() or None
+
+
+def _refuse(t: torch.Tensor) -> None:
+    if t.numel():  # an empty tensor is never read
         if not t.is_cuda:
             raise ValueError("tensor must be on a CUDA device")
         if t.get_device() != torch.cuda.current_device():
@@ -157,11 +170,12 @@ def _ptr(t: torch.Tensor | None):
                              f"cuda:{torch.cuda.current_device()}")
         if not t.is_contiguous():
             raise ValueError("tensor must be contiguous (the library reads rows at the strides it is given)")
-    return t.data_ptr() or None
 
 
 def _stream(stream) -> int:
     if stream is None:
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -394,15 +408,13 @@ def kv_copy_blocks(pools, src_blocks, dst_blocks, num_pairs, num_blocks, stream=
     sequence of tensors of num_blocks blocks each (every layer's caches and
     scales). Pairs with a negative id are padding."""
     n = len(pools)
-    bases, sizes = (ctypes.c_void_p * n)(), (ctypes.c_size_t * n)()
-    for i, t in enumerate(pools):
-        bases[i] = _ptr(t)
-        nbytes = t.numel() * t.element_size()
-        if num_blocks <= 0 or nbytes % num_blocks:
+    bases = [_ptr(t) for t in pools]
+    sizes = [t.nbytes for t in pools]
+    for i, size in enumerate(sizes):
+        if num_blocks <= 0 or size % num_blocks:
             raise ValueError(f"pool {i} does not hold {num_blocks} equal blocks")
-        sizes[i] = nbytes // num_blocks
     _check("kv_copy_blocks", lib().kv_copy_blocks(
-        bases, sizes, n, _ptr(src_blocks), _ptr(dst_blocks), num_pairs, num_blocks, _stream(stream)))
+        (ctypes.c_void_p * n)(*bases), (ctypes.c_size_t * n)(*[size // num_blocks for size in sizes]), n, _ptr(src_blocks), _ptr(dst_blocks), num_pairs, num_blocks, _stream(stream)))
 
 
 def kv_free_blocks(block_tables, ref_counts, first_block, end_block, max_blocks_per_seq, num_seqs, num_blocks,

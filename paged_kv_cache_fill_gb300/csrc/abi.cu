@@ -18,7 +18,6 @@ std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
 void* g_ws_ptr[kMaxDevices];
 size_t g_ws_bytes[kMaxDevices];
-bool g_ws_fresh[kMaxDevices];
 
 int current_device() {
   int d = 0;
@@ -191,12 +190,20 @@ int kv_write_fused_k_norm_rope_fp8(const kv_bf16_t* k_in, const kv_bf16_t* k_nor
                       stream);
 }
 
+// The longest piece of a sequence that one accumulator sums under split-KV, in
+// 16-position tiles. The tensor cores add to it towards zero, so its error grows
+// with the length of the sum: on 64 sequences of 32,768 positions (FP8, 8 heads of
+// 128) a CTA's whole share of 431 tiles is 7.8e-6 of the result off and takes 637
+// us, pieces of at most 256 are 4.0e-6 off and take 642, of 128 2.0e-6 and 651.
+// The calls without sinks sum a CTA's whole share in one.
+constexpr uint32_t kSumTiles = 256, kWholeShare = UINT32_MAX;
+
 static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_cache, float* output,
                          const int32_t* block_tables, const int32_t* seq_lens, uint32_t max_blocks_per_seq,
                          uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_dim,
                          uint32_t block_size, float inv_sqrt_d, float k_scale, uint32_t q_stride,
-                         uint32_t sliding_window, bool fp8, bool fp8_v, float v_scale, uint32_t num_sinks,
-                         bool block_scales, const float* k_scales, const float* v_scales, void* stream) {
+                         uint32_t sliding_window, bool fp8, bool fp8_v, float v_scale, uint32_t max_chunk_tiles,
+                         uint32_t num_sinks, bool block_scales, const float* k_scales, const float* v_scales, void* stream) {
   if (num_seqs == 0) return KV_OK;
   if (!q || !k_cache || !v_cache || !output || !block_tables || !seq_lens) return KV_ERR_INVALID_ARG;
   if (block_scales && (!k_scales || !v_scales)) return KV_ERR_INVALID_ARG;
@@ -237,6 +244,7 @@ static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_
   a.fp8 = fp8;
   a.fp8_v = fp8_v;
   a.v_scale = v_scale;
+  a.max_chunk_tiles = max_chunk_tiles;
   a.num_sinks = num_sinks;
   a.k_scales = k_scales;
   a.v_scales = v_scales;
@@ -244,16 +252,8 @@ static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_
     std::lock_guard<std::mutex> lock(g_mutex);
     a.workspace = g_ws_ptr[dev.device];
     a.workspace_bytes = g_ws_bytes[dev.device];
-    a.workspace_fresh = g_ws_fresh[dev.device];
   }
-  const int status = launch_decode(a, as_stream(stream));
-  if (status == KV_OK && a.workspace_fresh) {
-    // the work counters were zeroed on this call's stream; the kernels keep
-    // them at zero from here on
-    std::lock_guard<std::mutex> lock(g_mutex);
-    if (g_ws_ptr[dev.device] == a.workspace) g_ws_fresh[dev.device] = false;
-  }
-  return status;
+  return launch_decode(a, as_stream(stream));
 }
 
 int paged_decode_attn_bf16(const kv_bf16_t* q, const kv_bf16_t* k_cache, const kv_bf16_t* v_cache,
@@ -263,7 +263,8 @@ int paged_decode_attn_bf16(const kv_bf16_t* q, const kv_bf16_t* k_cache, const k
                            uint32_t q_stride, uint32_t sliding_window, void* stream) {
   return decode_common(q, k_cache, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
-                       sliding_window, false, false, 1.0f, 0, false, nullptr, nullptr, stream);
+                       sliding_window, false, false, 1.0f, kWholeShare, 0, false, nullptr,
+                       nullptr, stream);
 }
 
 int paged_decode_attn_fp8k(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_bf16_t* v_cache,
@@ -273,7 +274,8 @@ int paged_decode_attn_fp8k(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, con
                            float k_scale, uint32_t q_stride, uint32_t sliding_window, void* stream) {
   return decode_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, false, 1.0f, 0, false, nullptr, nullptr, stream);
+                       sliding_window, true, false, 1.0f, kWholeShare, 0, false, nullptr,
+                       nullptr, stream);
 }
 
 int paged_decode_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
@@ -284,7 +286,8 @@ int paged_decode_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, cons
                           void* stream) {
   return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, true, v_scale, 0, false, nullptr, nullptr, stream);
+                       sliding_window, true, true, v_scale, kWholeShare, 0, false, nullptr,
+                       nullptr, stream);
 }
 
 int paged_decode_attn_bf16_sinks(const kv_bf16_t* q, const kv_bf16_t* k_cache, const kv_bf16_t* v_cache,
@@ -294,7 +297,8 @@ int paged_decode_attn_bf16_sinks(const kv_bf16_t* q, const kv_bf16_t* k_cache, c
                                  uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks, void* stream) {
   return decode_common(q, k_cache, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
-                       sliding_window, false, false, 1.0f, num_sinks, false, nullptr, nullptr, stream);
+                       sliding_window, false, false, 1.0f, kSumTiles, num_sinks, false,
+                       nullptr, nullptr, stream);
 }
 
 int paged_decode_attn_fp8k_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_bf16_t* v_cache,
@@ -305,7 +309,8 @@ int paged_decode_attn_fp8k_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp
                                  void* stream) {
   return decode_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, false, 1.0f, num_sinks, false, nullptr, nullptr, stream);
+                       sliding_window, true, false, 1.0f, kSumTiles, num_sinks, false,
+                       nullptr, nullptr, stream);
 }
 
 int paged_decode_attn_fp8_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
@@ -316,7 +321,8 @@ int paged_decode_attn_fp8_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8
                                 uint32_t num_sinks, void* stream) {
   return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, true, v_scale, num_sinks, false, nullptr, nullptr, stream);
+                       sliding_window, true, true, v_scale, kSumTiles, num_sinks, false,
+                       nullptr, nullptr, stream);
 }
 
 int paged_decode_attn_fp8_block(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, const kv_e4m3_t* v_cache_fp8,
@@ -327,7 +333,8 @@ int paged_decode_attn_fp8_block(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8
                                 uint32_t num_sinks, void* stream) {
   return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
-                       sliding_window, true, true, 1.0f, num_sinks, true, k_scales, v_scales, stream);
+                       sliding_window, true, true, 1.0f, kSumTiles, num_sinks, true, k_scales,
+                       v_scales, stream);
 }
 
 static int prefill_common(const kv_bf16_t* q, const void* k_cache, const void* v_cache, void* output,
@@ -598,7 +605,6 @@ int kv_set_decode_workspace(void* device_ptr, size_t bytes) {
   std::lock_guard<std::mutex> lock(g_mutex);
   g_ws_ptr[d] = bytes ? device_ptr : nullptr;
   g_ws_bytes[d] = device_ptr ? bytes : 0;
-  g_ws_fresh[d] = g_ws_ptr[d] != nullptr;
   return KV_OK;
 }
 

@@ -68,8 +68,7 @@ namespace {
 __device__ uint32_t g_decode_error;
 
 constexpr int kTile = 16;            // tokens per stage
-constexpr int kHeaderBytes = 256;    // workspace header (work and done counters)
-constexpr int kChunksPerCta = 1;     // chunks of the tile stream per CTA
+constexpr int kHeaderBytes = 256;    // workspace header (unused; the sizes callers were told include it)
 constexpr int kMinChunkTiles = 4;    // smallest chunk: 64 positions
 constexpr int kSplitUnitTiles = 16;  // the workspace-size formula's split unit: 256 positions
 constexpr float kLog2e = 1.4426950408889634f;
@@ -94,7 +93,6 @@ struct DecodeParams {
   float* ws_o;          // [num_seqs, max_splits, Hq, D] partial outputs (unnormalised)
   float* ws_ml;         // [num_seqs, max_splits, Hq, 2] running max (log2 units) and sum
   uint32_t* ws_count;   // [num_seqs, num_head_groups] pieces of each (sequence, head group)
-  uint32_t* ws_header;  // [1] work counter, [2] done counter
   uint32_t max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, block_size, block_shift;
   uint32_t group;       // query heads per KV head
   uint32_t heads_per_item;  // HG
@@ -105,6 +103,7 @@ struct DecodeParams {
   const float* v_scales;
   uint32_t max_splits;  // 0: no workspace, one item per (sequence, head group)
   uint32_t min_chunk_tiles;  // chunks at least this long keep every sequence within max_splits pieces
+  uint32_t max_chunk_tiles;  // longest chunk (min_chunk_tiles permitting)
   float score_scale;    // inv_sqrt_d * log2(e)   (times k_scale for FP8)
   float out_scale;      // FP8 V: v_scale / 2^8 (P enters the MMA scaled by 2^8)
   uint32_t stages, stage_bytes, k_bytes, v_bytes;  // shared-memory ring geometry
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   StageMeta* meta = reinterpret_cast<StageMeta*>(empty + p.stages);
   // kBlk: a stage's K scales of the item's heads, then its V scales
   float* scales = reinterpret_cast<float*>(meta + p.stages);
-  __shared__ uint64_t s_chunk, s_total;
+  __shared__ uint64_t s_chunk, s_total, s_per_cta;
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t num_consumers = p.heads_per_item * NT;
@@ -294,8 +293,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   }
   __syncthreads();
 
-  // Chunk size: the stream's tiles over kChunksPerCta chunks per CTA, never
-  // below the minimum chunk (or the larger one a small workspace imposes).
+  // Chunk size: the stream's tiles over the CTAs, cut once more into equal
+  // chunks of at most max_chunk_tiles, never below the minimum chunk (or the
+  // larger one a small workspace imposes).
   if (p.max_splits > 0) {
     uint64_t local = 0;
     for (uint32_t s = threadIdx.x; s < p.num_seqs; s += blockDim.x)
@@ -306,8 +306,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
     __syncthreads();
     if (threadIdx.x == 0) {
       s_total *= p.num_head_groups;
-      const uint64_t parts = uint64_t(gridDim.x) * kChunksPerCta;
-      const uint64_t want = (s_total + parts - 1) / parts;
+      const uint64_t share = (s_total + gridDim.x - 1) / gridDim.x;
+      s_per_cta = share > p.max_chunk_tiles ? (share + p.max_chunk_tiles - 1) / p.max_chunk_tiles : 1;
+      const uint64_t want = (share + s_per_cta - 1) / s_per_cta;
       s_chunk = want > p.min_chunk_tiles ? want : p.min_chunk_tiles;
     }
     __syncthreads();
@@ -417,19 +418,17 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
     };
 
     if (p.max_splits > 0) {
-      // Stream-K: chunk k holds stream tiles [k C, (k + 1) C). CTA b takes
-      // chunk b; chunks past the grid (more than one per CTA) come from an
-      // atomic counter in the workspace header, in increasing order, so the
-      // walker only moves forward. The piece of (sequence, head group) range
-      // [a, b) that lies in chunk k is its piece k - floor(a / C).
+      // Stream-K: chunk k holds stream tiles [k C, (k + 1) C), and CTA b takes
+      // chunks b n .. b n + n - 1 (n = s_per_cta), so the walker only moves
+      // forward. The piece of (sequence, head group) range [a, b) that lies in
+      // chunk k is its piece k - floor(a / C).
       const uint64_t C = s_chunk, total = s_total;
       const uint64_t nchunks = (total + C - 1) / C;
-      uint32_t* const work = p.ws_header + 1;
       Walker wk;
       wk.chunk_base = 0;
       wk.load(0, p, lane);
-      uint64_t k = blockIdx.x;
-      while (ok && k < nchunks) {
+      const uint64_t k1 = (uint64_t(blockIdx.x) + 1) * s_per_cta;
+      for (uint64_t k = uint64_t(blockIdx.x) * s_per_cta; ok && k < k1 && k < nchunks; ++k) {
         uint64_t g = k * C;
         const uint64_t g1 = g + C < total ? g + C : total;
         while (ok && g < g1) {
@@ -453,8 +452,6 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           emit(s, hg, split, span, int32_t(g - a), int32_t(e - a), (g == a && e == b) ? kSingle : 0);
           g = e;
         }
-        if (nchunks <= gridDim.x) break;
-        k = gridDim.x + __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(work, 1u) : 0u, 0);
       }
     } else {
       // no workspace: whole (sequence, head group) items, statically strided
@@ -491,14 +488,6 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       for (uint32_t st = 0; st < p.stages; ++st)
         if ((issued >> st) & 1u)
           if (!mbar_wait(&full[st], (issued_parity >> st) & 1u)) atomicOr(&g_decode_error, kErrWaitTimeout);
-    }
-    // The last CTA to finish resets the counters for the next launch.
-    if (p.max_splits > 0 && lane == 0) {
-      __threadfence();
-      if (atomicAdd(p.ws_header + 2, 1u) == gridDim.x - 1) {
-        atomicExch(p.ws_header + 1, 0u);
-        atomicExch(p.ws_header + 2, 0u);
-      }
     }
     return;
   }
@@ -1054,6 +1043,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   // workspace holds fewer pieces per sequence than that needs.
   const uint64_t max_tiles = (uint64_t(a.max_blocks_per_seq) * a.block_size + kTile - 1) / kTile;
   const uint64_t fixed = kHeaderBytes + count_bytes(a.num_seqs, a.num_kv_heads);
+  p.max_chunk_tiles = a.max_chunk_tiles;
   p.max_splits = 0;
   p.min_chunk_tiles = 0;
   if (a.workspace && a.workspace_bytes > fixed && max_tiles > 1) {
@@ -1065,13 +1055,9 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     else if (fit >= 2)
       c = (max_tiles - 2) / (fit - 1) + 1;  // the least c with max_pieces(max_tiles, c) <= fit
     if (c) {
-      if (a.workspace_fresh &&
-          cudaMemsetAsync(a.workspace, 0, kHeaderBytes, stream) != cudaSuccess)
-        return KV_ERR_CUDA;
       p.min_chunk_tiles = uint32_t(c);
       p.max_splits = uint32_t(max_pieces(max_tiles, c));
       uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-      p.ws_header = reinterpret_cast<uint32_t*>(ws);
       p.ws_count = reinterpret_cast<uint32_t*>(ws + kHeaderBytes);
       p.ws_o = reinterpret_cast<float*>(ws + fixed);
       p.ws_ml = p.ws_o + uint64_t(a.num_seqs) * p.max_splits * a.num_q_heads * a.head_dim;

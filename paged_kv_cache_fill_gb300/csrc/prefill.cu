@@ -773,48 +773,49 @@ __global__ void __launch_bounds__(32 * 12, 1)
     // under a window the row skips the keys [num_sinks, pos + 1 - W)
     const int32_t lo = W > 0 ? pos + 1 - W : INT32_MIN;
     const uint32_t skipped = lo > p.num_sinks ? uint32_t(lo - p.num_sinks) : 0u;
-    // the Q row into the tile's shared-memory tile ([chunk][row][128 B],
-    // 128-byte swizzled), zeros past the item. E4M3 K cache: the row as f16,
-    // times 2^e with e chosen so that its largest magnitude lies in
-    // [2^14, 2^15) (exact for BF16 values in range), and the row's score
+    // The warp's 32 Q rows into the tile's shared-memory tile ([chunk][row][128
+    // B], 128-byte swizzled), zeros past the item. D / 8 lanes take a row
+    // together, so that a load covers whole rows (a row per thread, 32 rows'
+    // 16-byte pieces to a load, took 5.5 us of an item's first 9 us). E4M3 K cache:
+    // the row as f16, times 2^e with e chosen so that its largest magnitude
+    // lies in [2^14, 2^15) (exact for BF16 values in range; e at most 126, so
+    // that 2^e and 2^-e stay normal for subnormal rows), and the row's score
     // scale rs undoes 2^e.
     float rs = p.score_scale;
     {
-      const uint16_t* qr = valid ? p.q + uint64_t(it.qstart + tok) * p.q_stride + uint64_t(it.kv_head * g + hh) * D
-                                 : nullptr;
+      constexpr uint32_t kLanes = D / 8, kPer = 32 / kLanes;  // lanes per row, rows per load
+      const int64_t off = valid ? int64_t(uint64_t(it.qstart + tok) * p.q_stride + uint64_t(it.kv_head * g + hh) * D) : -1;
       uint8_t* qt = smem + Lay::kQ0 + t * Lay::kQBytes;
-      uint4 qv[D / 8];
+      const uint32_t u = lane % kLanes;  // the 16-byte unit of the row
+      uint4 qv[kLanes];
 #pragma unroll
-      for (uint32_t u = 0; u < D / 8; ++u)
-        qv[u] = qr ? *reinterpret_cast<const uint4*>(qr + 8 * u) : make_uint4(0, 0, 0, 0);
-      if constexpr (kFp8) {
-        float amax = 0.0f;
-#pragma unroll
-        for (uint32_t u = 0; u < D / 8; ++u) {
-          const uint32_t w4[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            amax = fmaxf(amax, fmaxf(fabsf(bf16_lo_to_f32(w4[q])), fabsf(bf16_hi_to_f32(w4[q]))));
-        }
-        int e = 0;
-        if (amax > 0.0f && amax < INFINITY) {
-          int ex;
-          frexpf(amax, &ex);
-          e = 15 - ex < 126 ? 15 - ex : 126;  // 2^e and 2^-e stay normal for subnormal rows
-        }
-        const float sc = ldexpf(1.0f, e);
-        rs = p.score_scale * ldexpf(1.0f, -e);
-#pragma unroll
-        for (uint32_t u = 0; u < D / 8; ++u) {
-          uint32_t w4[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) w4[q] = f32x2_to_f16x2(bf16_lo_to_f32(w4[q]) * sc, bf16_hi_to_f32(w4[q]) * sc);
-          qv[u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-        }
+      for (uint32_t i = 0; i < kLanes; ++i) {
+        const int64_t o = __shfl_sync(0xffffffffu, off, i * kPer + lane / kLanes);
+        qv[i] = o >= 0 ? *reinterpret_cast<const uint4*>(p.q + o + 8 * u) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (uint32_t u = 0; u < D / 8; ++u)  // 16-byte unit u: chunk u / 8, unit u % 8 of its 128-byte row
-        *reinterpret_cast<uint4*>(qt + (u >> 3) * (kTcBM * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = qv[u];
+      for (uint32_t i = 0; i < kLanes; ++i) {
+        const uint32_t r2 = (warp & 3) * 32 + i * kPer + lane / kLanes;  // the row of this lane's unit
+        if constexpr (kFp8) {
+          // the largest |q| of the row as a BF16 pattern
+          uint32_t m = __vmaxu2(__vmaxu2(qv[i].x & 0x7fff7fffu, qv[i].y & 0x7fff7fffu),
+                                __vmaxu2(qv[i].z & 0x7fff7fffu, qv[i].w & 0x7fff7fffu));
+          m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+          for (uint32_t o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          int32_t e = 15 - (int32_t(m >> 7) - 126);
+          e = m == 0 || m >= 0x7f80u ? 0 : e < 126 ? e : 126;
+          const float sc = __uint_as_float(uint32_t(e + 127) << 23);
+          uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w4[q] = f32x2_to_f16x2(bf16_lo_to_f32(w4[q]) * sc, bf16_hi_to_f32(w4[q]) * sc);
+          qv[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          const int32_t mine = __shfl_sync(0xffffffffu, e, (lane % kPer) * kLanes);
+          if (lane / kPer == i) rs = p.score_scale * __uint_as_float(uint32_t(127 - mine) << 23);
+        }
+        // 16-byte unit u: chunk u / 8, unit u % 8 of its 128-byte row
+        *reinterpret_cast<uint4*>(qt + (u >> 3) * (kTcBM * 128) + r2 * 128 + (((u & 7) ^ (r2 & 7)) << 4)) = qv[i];
+      }
     }
     fence_async_smem();
     mbar_arrive(&q_full);

@@ -109,8 +109,6 @@ extern "C" int paged_decode_attn_fp8k_static_scratch(
   a.fp8 = true;
   a.workspace = scratch;
   a.workspace_bytes = kStaticScratchBytes;
-  // The array keeps whatever the previous call left in it: have the decode
-  // clear its work counters on this call's stream before it starts.
-  a.workspace_fresh = true;
+  a.max_chunk_tiles = UINT32_MAX;
   return launch_decode(a, static_cast<cudaStream_t>(stream));
 }
