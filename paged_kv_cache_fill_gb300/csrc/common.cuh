@@ -272,10 +272,17 @@ __device__ __forceinline__ void bulk_store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// Arrive on `bar` once all tcgen05 operations this thread issued so far are done.
+// The MMAs and their commits are called by a whole converged warp, one elected
+// lane (always the same) issuing them: in a branch of one lane the compiler
+// cannot keep the descriptors in uniform registers, and moving them there for each
+// MMA bounds the issue (128 x 128 x 16: 62 to 150 cycles each, as much code as
+// lies around them; 58 like this, where the tensor pipe takes 64).
+// Arrive on `bar` once all tcgen05 operations the elected lane issued so far are done.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 // 32 consecutive 32-bit TMEM columns of this thread's lane (warp-wide).
@@ -308,22 +315,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem desc], one thread: A (M x K) in tensor
+// D[tmem] (+)= A[tmem] * B[smem desc]: A (M x K) in tensor
 // memory, row m in lane m, two K elements per 32-bit column (the lower in the
 // low half). kind::f16: A and B both BF16 or both f16, as idesc says.
 __device__ __forceinline__ void umma_f16kind_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t b_desc,
                                                     uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
       "r"(tmem_a), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
-// D[tmem] (+)= A[smem desc] * B[smem desc], one thread; kind::f16 as above.
+// D[tmem] (+)= A[smem desc] * B[smem desc]; kind::f16 as above.
 __device__ __forceinline__ void umma_f16kind_ss(uint32_t tmem_d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                 bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -350,6 +357,13 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
+}
+
+// A float (not NaN) as BF16, rounded towards +infinity.
+__device__ __forceinline__ uint16_t bf16_up(float x) {
+  const uint32_t b = __float_as_uint(x);
+  // up in magnitude where positive, down where negative: add the dropped bits' room, or drop them
+  return uint16_t((int32_t(b) >= 0 ? b + 0xffffu : b) >> 16);
 }
 
 __device__ __forceinline__ float bf16_lo_to_f32(uint32_t v) { return __uint_as_float(v << 16); }

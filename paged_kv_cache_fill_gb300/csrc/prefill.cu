@@ -46,6 +46,7 @@ struct PrefillParams {
   uint32_t max_blocks_per_seq, num_seqs, num_q_tokens, num_q_heads, num_kv_heads, group;
   uint32_t block_size, block_shift, q_stride, sliding_window;
   int32_t num_sinks;      // first positions that stay visible under a window
+  int32_t key_align;      // where an item's window may begin: 16, or 128 keys
   uint32_t bf16_out;
   const float* k_scales;  // kBlk: [num_blocks, num_kv_heads]
   const float* v_scales;
@@ -140,12 +141,21 @@ __device__ __forceinline__ uint32_t len_class(uint64_t tiles) {
   return c < kLenClasses ? c : kLenClasses - 1;
 }
 
-// Tiles of the sinks below a window that begins at key k_lo: those before the
-// window's first tile (which covers the sinks that lie in it).
-__device__ __forceinline__ int64_t sink_tiles(int32_t num_sinks, int64_t k_lo) {
-  const int64_t s = num_sinks < k_lo ? num_sinks : k_lo;
-  const int64_t t = (s + kTcBN - 1) / kTcBN;
-  return t < k_lo / kTcBN ? t : k_lo / kTcBN;
+// The keys that an item of the window [k_lo, k_hi) reads, as one list: the sinks
+// in whole boxes of 16 keys, [0, sinks16), then from the window's first box on,
+// so that tiles of 128 list places hold what some row attends and little else
+// (a tile of sinks and a window begun at a multiple of 128 keys cost 10.5 tiles
+// where a window of 1024 and four sinks now take 9). Place c holds key c, or c +
+// delta from sinks16 on. The calls without sinks begin their window at a multiple
+// of 128 keys, as they did.
+struct KeyList {
+  int32_t sinks16, delta;
+};
+__device__ __forceinline__ KeyList key_list(const PrefillParams& p, int32_t k_lo) {
+  const int32_t w0 = k_lo / p.key_align * p.key_align;
+  const int32_t s = p.num_sinks < k_lo ? p.num_sinks : k_lo, s16 = (s + kSub - 1) / kSub * kSub;
+  const int32_t sinks16 = s16 < w0 ? s16 : w0;
+  return KeyList{sinks16, w0 - sinks16};
 }
 
 // Sequence s's share of the item list: its query tokens n, its items (row
@@ -169,7 +179,7 @@ __device__ __forceinline__ uint32_t seq_items(const PrefillParams& p, uint32_t s
   L = L < 0 ? 0 : (L > cap ? cap : L);
   int64_t k_lo = 0;
   if (p.sliding_window > 0 && L - n + 1 - int64_t(p.sliding_window) > 0) k_lo = L - n + 1 - p.sliding_window;
-  const int64_t tiles = (L + kTcBN - 1) / kTcBN - k_lo / kTcBN + sink_tiles(p.num_sinks, k_lo);
+  const int64_t tiles = (L - key_list(p, int32_t(k_lo)).delta + kTcBN - 1) / kTcBN;
   cls = len_class(tiles > 0 ? uint64_t(tiles) : 0);
   return row_blocks<BM>(n, p.group) * p.num_kv_heads;
 }
@@ -180,6 +190,44 @@ template <int BM>
 __device__ Item locate(uint32_t target, const PrefillParams& p, uint32_t lane, uint32_t* hist) {
   Item it{};
   it.seq = -1;
+  // item `local` of sequence `seq` (n query tokens)
+  auto take = [&](uint32_t seq, uint32_t local, int64_t n) {
+    const uint32_t nblk = row_blocks<BM>(n, p.group);
+    const uint32_t blk = nblk - 1 - local / p.num_kv_heads;  // longest key range first
+    it.seq = int32_t(seq);
+    it.kv_head = int32_t(local % p.num_kv_heads);
+    it.row0 = int32_t(blk * BM);
+    const int64_t rows_total = n * p.group;
+    it.rows = int32_t(rows_total - it.row0 < BM ? rows_total - it.row0 : BM);
+    it.n = int32_t(n);
+    it.qstart = __ldg(p.qsl + it.seq);
+    int32_t L = __ldg(p.seq_lens + it.seq);
+    if (L < 0) L = 0;
+    const int64_t cap = int64_t(p.max_blocks_per_seq) << p.block_shift;
+    if (L > cap) {
+      L = int32_t(cap);
+      if (lane == 0 && it.kv_head == 0) atomicOr(&g_prefill_error, kErrSeqLenClamped);
+    }
+    it.len = L;
+  };
+  if (p.num_seqs <= 32) {
+    // a sequence per lane: the items before a lane's own in one pass, without
+    // the histogram (2.0 -> 1.4 us of each CTA's start)
+    int64_t n;
+    uint32_t cls;
+    const uint32_t items = seq_items<BM>(p, lane, true, n, cls);
+    uint64_t before = 0;
+    for (uint32_t m = 0; m < p.num_seqs; ++m) {
+      const uint32_t im = __shfl_sync(0xffffffffu, items, m), cm = __shfl_sync(0xffffffffu, cls, m);
+      if (cm > cls || (cm == cls && m < lane)) before += im;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, target >= before && target - before < items);
+    if (hit) {
+      const uint32_t sl = __ffs(hit) - 1;
+      take(sl, uint32_t(target - __shfl_sync(0xffffffffu, before, sl)), __shfl_sync(0xffffffffu, n, sl));
+    }
+    return it;
+  }
   for (uint32_t c = lane; c < kLenClasses; c += 32) hist[c] = 0;
   __syncwarp();
   // items per length class
@@ -232,24 +280,7 @@ __device__ Item locate(uint32_t target, const PrefillParams& p, uint32_t lane, u
       const uint32_t sl = __ffs(__ballot_sync(0xffffffffu, incl > uint32_t(rel))) - 1;
       const uint32_t local =
           uint32_t(rel) - (__shfl_sync(0xffffffffu, incl, sl) - __shfl_sync(0xffffffffu, items, sl));
-      const int64_t ns = __shfl_sync(0xffffffffu, n, sl);
-      const uint32_t nblk = row_blocks<BM>(ns, p.group);
-      const uint32_t blk = nblk - 1 - local / p.num_kv_heads;  // longest key range first
-      it.seq = int32_t(s0 + sl);
-      it.kv_head = int32_t(local % p.num_kv_heads);
-      it.row0 = int32_t(blk * BM);
-      const int64_t rows_total = ns * p.group;
-      it.rows = int32_t(rows_total - it.row0 < BM ? rows_total - it.row0 : BM);
-      it.n = int32_t(ns);
-      it.qstart = __ldg(p.qsl + it.seq);
-      int32_t L = __ldg(p.seq_lens + it.seq);
-      if (L < 0) L = 0;
-      const int64_t cap = int64_t(p.max_blocks_per_seq) << p.block_shift;
-      if (L > cap) {
-        L = int32_t(cap);
-        if (lane == 0 && it.kv_head == 0) atomicOr(&g_prefill_error, kErrSeqLenClamped);
-      }
-      it.len = L;
+      take(s0 + sl, local, __shfl_sync(0xffffffffu, n, sl));
       return it;
     }
     rel -= total;
@@ -412,31 +443,31 @@ __global__ void __launch_bounds__(32 * 12, 1)
     const Item it = locate<kTc2Rows>(blockIdx.x, p, lane, reinterpret_cast<uint32_t*>(smem));  // (free until the Q rows)
     if (lane == 0) s_item = it;
   }
-  __syncthreads();
-  const Item it = s_item;
-  if (it.seq < 0) return;
   if (warp == 1) tmem_alloc(&tmem_base_s, Lay::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const Item it = s_item;
   const uint32_t tmem = tmem_base_s;
+  if (it.seq < 0) {  // past the last item
+    if (warp == 1) tmem_dealloc(tmem, Lay::kTmemCols);
+    return;
+  }
 
   const int32_t g = int32_t(p.group);
   const bool two = it.rows > kTcBM;  // tile B holds rows
   const int32_t pos_first = it.len - it.n + it.row0 / g;
-  const int32_t pos_last = it.len - it.n + (it.row0 + it.rows - 1) / g;
-  const int32_t k_hi = pos_last + 1;  // keys [k_lo, k_hi)
   const int32_t W = int32_t(p.sliding_window);
-  int32_t k_lo = 0;
-  if (W > 0 && pos_first + 1 - W > 0) k_lo = pos_first + 1 - W;
-  const int32_t t_begin = k_lo / kTcBN;
-  const int32_t t_end = k_hi > 0 ? (k_hi + kTcBN - 1) / kTcBN : t_begin;
-  // the item's key tiles: the sinks' ones, then those from the window's first;
-  // no row of the item attends the keys [dead_lo, k_lo)
-  const int32_t nsk = int32_t(sink_tiles(p.num_sinks, k_lo));
-  const int32_t T = t_end - t_begin + nsk;
-  const int32_t dead_lo = p.num_sinks < k_lo ? p.num_sinks : k_lo;
-  auto key_base_of = [&](int32_t i) { return (i < nsk ? i : t_begin + i - nsk) * kTcBN; };
+  const int32_t win_lo = W > 0 && pos_first + 1 - W > 0 ? pos_first + 1 - W : 0;
+  const KeyList list = key_list(p, win_lo);
+  // From here on positions are places in the list: keys [k_lo, k_hi) of the
+  // window and [0, dead_lo) of the sinks; no row of the item attends the keys
+  // [dead_lo, k_lo), which share boxes with those.
+  const int32_t pos_last = it.len - it.n + (it.row0 + it.rows - 1) / g - list.delta;
+  const int32_t k_hi = pos_last + 1, k_lo = win_lo - list.delta;
+  const int32_t dead_lo = p.num_sinks < win_lo ? p.num_sinks : win_lo;
+  const int32_t T = k_hi > 0 ? (k_hi + kTcBN - 1) / kTcBN : 0;
+  auto key_base_of = [&](int32_t i) { return i * kTcBN; };
 
   if (warp < 4) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(tc2_regs_low<kFp8V>()));
@@ -496,11 +527,11 @@ __global__ void __launch_bounds__(32 * 12, 1)
     const int32_t* table = p.block_tables + uint64_t(it.seq) * p.max_blocks_per_seq;
     bool ok = true;
     int32_t issued = 0;
-    // the box of tile i that this lane loads: 16 keys, unless no row of the
-    // item attends any of them (whose page may be gone)
+    // the first key of the box of tile i that this lane loads, if any
     auto my_box = [&](int32_t i, int32_t& key0) -> bool {
-      key0 = key_base_of(i) + int32_t(lane) * kSub;
-      return lane < uint32_t(kTcBN / kSub) && key0 < k_hi && !(key0 >= dead_lo && key0 + kSub <= k_lo);
+      const int32_t c = i * kTcBN + int32_t(lane) * kSub;
+      key0 = c < list.sinks16 ? c : c + list.delta;
+      return lane < uint32_t(kTcBN / kSub) && c < k_hi;
     };
     // kBlk: this lane's group's scales, loaded a tile ahead (1 where no box is
     // loaded). A negative block id (outside the caller's contract; its box is
@@ -675,7 +706,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
     if (!ok && lane == 0) atomicOr(&g_prefill_error, kErrWaitTimeout);
    } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
+    {
       // S: BF16 Q and K, or f16 Q rows scaled by powers of two against K converted to f16
       constexpr uint32_t idesc_s =
           kFp8 ? umma_idesc_f16(kTcBM, kTcBN, false) : umma_idesc_bf16(kTcBM, kTcBN, false);
@@ -687,7 +718,9 @@ __global__ void __launch_bounds__(32 * 12, 1)
       constexpr uint64_t kStageStep = Lay::kStageBytes >> 4;
       constexpr uint64_t kQStep = Lay::kQBytes >> 4;
       const uint32_t ntiles = two ? 2u : 1u;
-      bool ok = mbar_wait(&q_full, 0);
+      // (the whole warp, converged: see umma_commit)
+      auto wait = [](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+      bool ok = wait(&q_full, 0);
       tc_fence_after();
       // S_t(j) = Q_t K(j)^T into tile t's S columns
       auto issue_s = [&](int32_t j, uint32_t t) {
@@ -702,7 +735,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
         umma_commit(&s_full[t]);
       };
       if (ok && T > 0) {
-        ok = mbar_wait(&k_full[0], 0);
+        ok = wait(&k_full[0], 0);
         tc_fence_after();
         if (ok) {
           for (uint32_t t = 0; t < ntiles; ++t) issue_s(0, t);
@@ -717,13 +750,13 @@ __global__ void __launch_bounds__(32 * 12, 1)
         const uint32_t st = uint32_t(j) % kTcStages;
         const bool more = j + 1 < T;
         const uint32_t sn = uint32_t(j + 1) % kTcStages;
-        if (!mbar_wait(&v_full[st], uint32_t(j / kTcStages) & 1)) {
+        if (!wait(&v_full[st], uint32_t(j / kTcStages) & 1)) {
           ok = false;
           break;
         }
         const uint64_t vd = v_desc0 + st * kStageStep;
         for (uint32_t t = 0; t < ntiles && ok; ++t) {
-          if (!mbar_wait(&p_full[t], uint32_t(j) & 1)) {
+          if (!wait(&p_full[t], uint32_t(j) & 1)) {
             ok = false;
             break;
           }
@@ -738,11 +771,11 @@ __global__ void __launch_bounds__(32 * 12, 1)
           if (t + 1 == ntiles) umma_commit(&v_empty[st]);
           if (more) {
             // tile t's S columns hold P_t(j) until PV_t(j) is done
-            if (t == 0 && !mbar_wait(&k_full[sn], uint32_t((j + 1) / kTcStages) & 1)) {
+            if (t == 0 && !wait(&k_full[sn], uint32_t((j + 1) / kTcStages) & 1)) {
               ok = false;
               break;
             }
-            if (!mbar_wait(&o_full[t], uint32_t(j) & 1)) {
+            if (!wait(&o_full[t], uint32_t(j) & 1)) {
               ok = false;
               break;
             }
@@ -752,10 +785,10 @@ __global__ void __launch_bounds__(32 * 12, 1)
           }
         }
       }
-      if (!ok) atomicOr(&g_prefill_error, kErrWaitTimeout);
+      if (!ok && lane == 0) atomicOr(&g_prefill_error, kErrWaitTimeout);
       // every issued MMA has finished before TMEM is released
       umma_commit(&mma_done);
-      mbar_wait(&mma_done, 0);
+      wait(&mma_done, 0);
     }
     __syncwarp();
    }
@@ -769,8 +802,10 @@ __global__ void __launch_bounds__(32 * 12, 1)
     const bool valid = r < it.rows;
     const int32_t grow = it.row0 + r;
     const int32_t tok = grow / g, hh = grow % g;
-    const int32_t pos = valid ? it.len - it.n + tok : -1;  // -1: attends nothing
-    // under a window the row skips the keys [num_sinks, pos + 1 - W)
+    // a row past the item (zeros, not stored) is masked as its last row is
+    const int32_t pos = valid ? it.len - it.n + tok - list.delta : pos_last;
+    // under a window the row skips the places [num_sinks, pos + 1 - W) (place
+    // num_sinks holds that key wherever it is in the list)
     const int32_t lo = W > 0 ? pos + 1 - W : INT32_MIN;
     const uint32_t skipped = lo > p.num_sinks ? uint32_t(lo - p.num_sinks) : 0u;
     // The warp's 32 Q rows into the tile's shared-memory tile ([chunk][row][128
@@ -1130,6 +1165,7 @@ int launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   p.q_stride = a.q_stride;
   p.sliding_window = a.sliding_window;
   p.num_sinks = a.num_sinks > uint32_t(INT32_MAX) ? INT32_MAX : int32_t(a.num_sinks);
+  p.key_align = a.bf16_out ? kSub : kTcBN;
   p.bf16_out = a.bf16_out;
   p.k_scales = a.k_scales;
   p.v_scales = a.v_scales;

@@ -353,8 +353,9 @@ def test_queries_before_the_first_position_give_zeros(kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_sinks_change_nothing_without_a_window(kind):
-    """num_sinks without a window, and a window with no sinks, give the plain calls' bits (BF16 rows: their
-    rounding)."""
+    """num_sinks without a window gives the plain calls' bits (BF16 rows: their rounding). With a window and no sinks
+    the decode does too; the prefill begins its key tiles elsewhere, so that both are within the weights' rounding of
+    the same value (2 max|v| 2^-11 each, and the sums' 2^-18), `out` rounded to BF16 besides."""
     rng = np.random.default_rng(4)
     lens, new = np.array([300, 17]), np.array([50, 17])
     pool = Pool(rng, kind, lens, new, 2, 128, 16, 0, 0)
@@ -380,7 +381,13 @@ def test_sinks_change_nothing_without_a_window(kind):
         call(pool, "prefill", q, out, lens, [0, 50, 67], 4, W, 0)
         one = torch.empty((2, 4, 128), device=DEV)
         call(pool, "decode", q[:2], one, lens, None, 4, W, 0)
-        assert torch.equal(pre.to(torch.bfloat16), out) and torch.equal(dec, one)
+        assert torch.equal(dec, one)
+        if W == 0:
+            assert torch.equal(pre.to(torch.bfloat16), out)
+        else:
+            vmax = max(np.abs(v).max() for v in pool.rows[1])
+            tol = 4 * vmax * (2.0 ** -11 + 2.0 ** -18) + 2.0 ** -8 * pre.abs() + 2.0 ** -16
+            assert bool(((pre - out.float()).abs() <= tol).all())
 
 
 def test_calls_in_a_captured_graph():
