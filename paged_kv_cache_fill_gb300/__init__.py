@@ -14,6 +14,7 @@ integer, or None for torch's current stream.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -407,14 +408,20 @@ def kv_copy_blocks(pools, src_blocks, dst_blocks, num_pairs, num_blocks, stream=
     """Copy block src_blocks[i] to dst_blocks[i] in every one of `pools`, a
     sequence of tensors of num_blocks blocks each (every layer's caches and
     scales). Pairs with a negative id are padding."""
-    n = len(pools)
-    bases = [_ptr(t) for t in pools]
+    dev = _device()
+    for t in pools:  # (as _ptr does, which would cost a call per pool: a model has hundreds)
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("expected a torch.Tensor")
+        if t.get_device() != dev or not t.is_contiguous():
+            _refuse(t)
+    bases = array.array("Q", [t.data_ptr() for t in pools])
     sizes = [t.nbytes for t in pools]
     for i, size in enumerate(sizes):
         if num_blocks <= 0 or size % num_blocks:
             raise ValueError(f"pool {i} does not hold {num_blocks} equal blocks")
+    sizes = array.array("Q", [size // num_blocks for size in sizes])
     _check("kv_copy_blocks", lib().kv_copy_blocks(
-        (ctypes.c_void_p * n)(*bases), (ctypes.c_size_t * n)(*[size // num_blocks for size in sizes]), n, _ptr(src_blocks), _ptr(dst_blocks), num_pairs, num_blocks, _stream(stream)))
+        bases.buffer_info()[0], sizes.buffer_info()[0], len(bases), _ptr(src_blocks), _ptr(dst_blocks), num_pairs, num_blocks, _stream(stream)))
 
 
 def kv_free_blocks(block_tables, ref_counts, first_block, end_block, max_blocks_per_seq, num_seqs, num_blocks,
