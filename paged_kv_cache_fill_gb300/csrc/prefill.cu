@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
   __shared__ uint64_t k_full[kTcStages], v_full[kTcStages], k_empty[kTcStages], v_empty[kTcStages];
   __shared__ uint64_t k8_full[kTcStages], k8_empty[kTcStages];  // E4M3 K: loaded, read by the converter
   __shared__ uint64_t v8_full[kTcStages];                        // E4M3 V: loaded
-  __shared__ uint64_t s_full[2], p_full[2], o_full[2];  // per Q tile
+  __shared__ uint64_t s_full[2], p_full[2][2], o_full[2];  // per Q tile (P: and half of the keys)
   __shared__ uint64_t q_full, mma_done;
   __shared__ uint64_t sc_full[kBlk ? kScaleSlots : 1];  // kBlk: a tile's scales are in their slot
   __shared__ __align__(16) float sc_k[kBlk ? kScaleSlots : 1][kGroups], sc_v[kBlk ? kScaleSlots : 1][kGroups],
@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], kTcBM);
+      mbar_init(&p_full[t][0], kTcBM);
+      mbar_init(&p_full[t][1], kTcBM);
       mbar_init(&o_full[t], 1);
     }
     if constexpr (kBlk)
@@ -756,7 +757,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
         }
         const uint64_t vd = v_desc0 + st * kStageStep;
         for (uint32_t t = 0; t < ntiles && ok; ++t) {
-          if (!wait(&p_full[t], uint32_t(j) & 1)) {
+          if (!wait(&p_full[t][0], uint32_t(j) & 1)) {
             ok = false;
             break;
           }
@@ -764,6 +765,13 @@ __global__ void __launch_bounds__(32 * 12, 1)
           const uint32_t pt = tmem + Lay::s_col(t);  // P of tile t: keys 2m, 2m + 1 in column m
 #pragma unroll
           for (int kk = 0; kk < kTcBN / 16; ++kk) {
+            if (kk == kTcBN / 32) {
+              if (!wait(&p_full[t][1], uint32_t(j) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
             const uint64_t v_k = vd + uint64_t(kk * (16 * 128) >> 4);
             umma_f16kind_tmem_a(tmem + Lay::o_col(t), pt + 8 * kk, v_k, idesc_o, j > 0 || kk > 0);
           }
@@ -974,6 +982,23 @@ __global__ void __launch_bounds__(32 * 12, 1)
         // by more than kRescaleLog2 (or on its first finite score)
         const float mx = (m_run == -INFINITY || tile_max > m_run + kRescaleLog2) ? fmaxf(m_run, tile_max) : m_run;
         const float mb = mx == -INFINITY ? 0.0f : mx;
+        const float al = fast_exp2(m_run - mb);
+        const bool rescale = j > 0 && __any_sync(0xffffffffu, mx != m_run);
+        if (rescale) {
+          // O changes only once PV_t(j - 1) is done
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], uint32_t(j - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (uint32_t c0 = 0; c0 < uint32_t(D); c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(ocol + c0, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * al);
+            tmem_st32(ocol + c0, ov);
+          }
+        }
         // the weights are formed as 2^7 P (<= 2^15), so that they stay above
         // f16's subnormal range down to P = 2^-21; the sum l takes the same
         // factor
@@ -1010,6 +1035,11 @@ __global__ void __launch_bounds__(32 * 12, 1)
               sum = fmaf(s01.x + s01.y, vi[2 * c + g2], sum);
             }
             tmem_st16(scol + 16 * c, pw);
+            if (c == 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(&p_full[t][0]);
+            }
           }
         } else {
           const F2 sc2 = f2_make(rs, rs), nmb2 = f2_make(-mbp, -mbp);
@@ -1026,32 +1056,20 @@ __global__ void __launch_bounds__(32 * 12, 1)
               pw[q] = f32x2_to_f16x2(e0, e1);
             }
             tmem_st16(scol + 16 * c, pw);
+            if (c == 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(&p_full[t][0]);
+            }
           }
           const float2 s01 = f2_split(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])));
           sum = s01.x + s01.y;
-        }
-        const float al = fast_exp2(m_run - mb);
-        const bool rescale = j > 0 && __any_sync(0xffffffffu, mx != m_run);
-        if (rescale) {
-          // O changes only once PV_t(j - 1) is done
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], uint32_t(j - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (uint32_t c0 = 0; c0 < uint32_t(D); c0 += 32) {
-            uint32_t ov[32];
-            tmem_ld32(ocol + c0, ov);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * al);
-            tmem_st32(ocol + c0, ov);
-          }
         }
         l_run = l_run * al + sum;
         m_run = mx;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[t]);
+        mbar_arrive(&p_full[t][1]);
         // the next V tile, off the path of this tile's PV product
         if (j + 1 < T) ok = convert_v(j + 1);
       }
