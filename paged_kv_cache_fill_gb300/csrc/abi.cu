@@ -190,19 +190,11 @@ int kv_write_fused_k_norm_rope_fp8(const kv_bf16_t* k_in, const kv_bf16_t* k_nor
                       stream);
 }
 
-// The longest piece of a sequence that one accumulator sums under split-KV, in
-// 16-position tiles. The tensor cores add to it towards zero, so its error grows
-// with the length of the sum: on 64 sequences of 32,768 positions (FP8, 8 heads of
-// 128) a CTA's whole share of 431 tiles is 7.8e-6 of the result off and takes 637
-// us, pieces of at most 256 are 4.0e-6 off and take 642, of 128 2.0e-6 and 651.
-// The calls without sinks sum a CTA's whole share in one.
-constexpr uint32_t kSumTiles = 256, kWholeShare = UINT32_MAX;
-
 static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_cache, float* output,
                          const int32_t* block_tables, const int32_t* seq_lens, uint32_t max_blocks_per_seq,
                          uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_dim,
                          uint32_t block_size, float inv_sqrt_d, float k_scale, uint32_t q_stride,
-                         uint32_t sliding_window, bool fp8, bool fp8_v, float v_scale, uint32_t max_chunk_tiles,
+                         uint32_t sliding_window, bool fp8, bool fp8_v, float v_scale, bool fine,
                          uint32_t num_sinks, bool block_scales, const float* k_scales, const float* v_scales, void* stream) {
   if (num_seqs == 0) return KV_OK;
   if (!q || !k_cache || !v_cache || !output || !block_tables || !seq_lens) return KV_ERR_INVALID_ARG;
@@ -244,7 +236,7 @@ static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_
   a.fp8 = fp8;
   a.fp8_v = fp8_v;
   a.v_scale = v_scale;
-  a.max_chunk_tiles = max_chunk_tiles;
+  a.fine = fine;
   a.num_sinks = num_sinks;
   a.k_scales = k_scales;
   a.v_scales = v_scales;
@@ -263,7 +255,7 @@ int paged_decode_attn_bf16(const kv_bf16_t* q, const kv_bf16_t* k_cache, const k
                            uint32_t q_stride, uint32_t sliding_window, void* stream) {
   return decode_common(q, k_cache, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
-                       sliding_window, false, false, 1.0f, kWholeShare, 0, false, nullptr,
+                       sliding_window, false, false, 1.0f, false, 0, false, nullptr,
                        nullptr, stream);
 }
 
@@ -274,7 +266,7 @@ int paged_decode_attn_fp8k(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, con
                            float k_scale, uint32_t q_stride, uint32_t sliding_window, void* stream) {
   return decode_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, false, 1.0f, kWholeShare, 0, false, nullptr,
+                       sliding_window, true, false, 1.0f, false, 0, false, nullptr,
                        nullptr, stream);
 }
 
@@ -286,7 +278,7 @@ int paged_decode_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, cons
                           void* stream) {
   return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, true, v_scale, kWholeShare, 0, false, nullptr,
+                       sliding_window, true, true, v_scale, false, 0, false, nullptr,
                        nullptr, stream);
 }
 
@@ -297,7 +289,7 @@ int paged_decode_attn_bf16_sinks(const kv_bf16_t* q, const kv_bf16_t* k_cache, c
                                  uint32_t q_stride, uint32_t sliding_window, uint32_t num_sinks, void* stream) {
   return decode_common(q, k_cache, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
-                       sliding_window, false, false, 1.0f, kSumTiles, num_sinks, false,
+                       sliding_window, false, false, 1.0f, true, num_sinks, false,
                        nullptr, nullptr, stream);
 }
 
@@ -309,7 +301,7 @@ int paged_decode_attn_fp8k_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp
                                  void* stream) {
   return decode_common(q, k_cache_fp8, v_cache, output, block_tables, seq_lens, max_blocks_per_seq, num_seqs,
                        num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, false, 1.0f, kSumTiles, num_sinks, false,
+                       sliding_window, true, false, 1.0f, true, num_sinks, false,
                        nullptr, nullptr, stream);
 }
 
@@ -321,7 +313,7 @@ int paged_decode_attn_fp8_sinks(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8
                                 uint32_t num_sinks, void* stream) {
   return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, k_scale, q_stride,
-                       sliding_window, true, true, v_scale, kSumTiles, num_sinks, false,
+                       sliding_window, true, true, v_scale, true, num_sinks, false,
                        nullptr, nullptr, stream);
 }
 
@@ -333,7 +325,7 @@ int paged_decode_attn_fp8_block(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8
                                 uint32_t num_sinks, void* stream) {
   return decode_common(q, k_cache_fp8, v_cache_fp8, output, block_tables, seq_lens, max_blocks_per_seq,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d, 1.0f, q_stride,
-                       sliding_window, true, true, 1.0f, kSumTiles, num_sinks, true, k_scales,
+                       sliding_window, true, true, 1.0f, true, num_sinks, true, k_scales,
                        v_scales, stream);
 }
 

@@ -365,13 +365,6 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   return d;
 }
 
-// A float (not NaN) as BF16, rounded towards +infinity.
-__device__ __forceinline__ uint16_t bf16_up(float x) {
-  const uint32_t b = __float_as_uint(x);
-  // up in magnitude where positive, down where negative: add the dropped bits' room, or drop them
-  return uint16_t((int32_t(b) >= 0 ? b + 0xffffu : b) >> 16);
-}
-
 __device__ __forceinline__ float bf16_lo_to_f32(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi_to_f32(uint32_t v) {
   return __uint_as_float(v & 0xFFFF0000u);

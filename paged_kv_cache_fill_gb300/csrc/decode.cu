@@ -73,6 +73,18 @@ constexpr int kMinChunkTiles = 4;    // smallest chunk: 64 positions
 constexpr int kSplitUnitTiles = 16;  // the workspace-size formula's split unit: 256 positions
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The calls with sinks or block scales hold their 32-bit results to a few
+// 2^-20 (`fine`), where the earlier calls, whose bits stay as they were, do not:
+//   - The tensor cores add to an accumulator towards zero, so the error of a sum
+//     grows with its length. Under split-KV one accumulator sums at most
+//     kSumTiles tiles: on 64 sequences of 32,768 positions (FP8, 8 heads of 128) a
+//     CTA's whole share of 431 tiles is 7.8e-6 of the result off and takes 637 us,
+//     pieces of at most 192 tiles are 2.9e-6 off and take 646 (128: 2.0e-6, 651).
+//   - With a BF16 V the weights enter as three BF16 parts instead of two
+//     (error 2^-26 instead of 2^-17): on 64 sequences under a window of 1,000 and
+//     four sinks 2.2e-6 -> 1.2e-6 in the same 47 us.
+constexpr uint32_t kSumTiles = 192;
+
 enum : int32_t {
   kFirst = 1,    // first tile of an item
   kLast = 2,     // last tile of an item
@@ -104,6 +116,7 @@ struct DecodeParams {
   uint32_t max_splits;  // 0: no workspace, one item per (sequence, head group)
   uint32_t min_chunk_tiles;  // chunks at least this long keep every sequence within max_splits pieces
   uint32_t max_chunk_tiles;  // longest chunk (min_chunk_tiles permitting)
+  uint32_t fine;             // BF16 V: weights in three parts
   float score_scale;    // inv_sqrt_d * log2(e)   (times k_scale for FP8)
   float out_scale;      // FP8 V: v_scale / 2^8 (P enters the MMA scaled by 2^8)
   uint32_t stages, stage_bytes, k_bytes, v_bytes;  // shared-memory ring geometry
@@ -184,7 +197,7 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t head_base, uint32_t row, 
 // -------------------------------------------------------------- O^T += V^T P^T
 // One 16-token tile of the PV product for one warp: acc[i] holds the 16-dim
 // block i of O^T (8 query-head columns). B fragments (bh*, bl*) are the hi and
-// lo parts of P^T; kMask zeroes the V values of masked positions (their rows
+// lo parts of P^T, bt* (with `three`, BF16 V) what they leave; kMask zeroes the V values of masked positions (their rows
 // may hold NaN), with vmask01 / vmask89 covering this lane's tokens 2c4, 2c4+1
 // and 2c4+8, 2c4+9.
 //   BF16 V: per 16-dim block one transposing ldmatrix (rows: 16 tokens).
@@ -196,8 +209,8 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t head_base, uint32_t row, 
 //     the accumulator rows come out in that order too.
 template <bool kFp8V, int D, bool kMask>
 __device__ __forceinline__ void pv_tile(float (&acc)[D / 16][4], uint32_t vbase, uint32_t row, uint32_t unit_lo,
-                                        uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1, uint32_t vmask01,
-                                        uint32_t vmask89) {
+                                        uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1, bool three,
+                                        uint32_t bt0, uint32_t bt1, uint32_t vmask01, uint32_t vmask89) {
   constexpr int kVRow = D * (kFp8V ? 1 : 2);  // bytes of one head's V row
   if constexpr (!kFp8V) {
     uint32_t a[D / 16][4];
@@ -215,6 +228,10 @@ __device__ __forceinline__ void pv_tile(float (&acc)[D / 16][4], uint32_t vbase,
     // the lo parts after every hi part: no MMA waits on the one before
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) mma_bf16(acc[i], a[i], bl0, bl1);
+    if (three) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) mma_bf16(acc[i], a[i], bt0, bt1);
+    }
   } else {
 #pragma unroll
     for (int jj = 0; jj < D / 32; ++jj) {
@@ -689,11 +706,17 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         vmask89 = (attended(q0 + 8) ? 0x0000ffffu : 0u) | (attended(q0 + 9) ? 0xffff0000u : 0u);
       }
       uint32_t bh0, bh1, bl0, bl1;
+      [[maybe_unused]] uint32_t bt0 = 0, bt1 = 0;
       if constexpr (!kFp8V) {
         // ---- P^T as B fragments: hi and lo BF16 parts, transposed by movmatrix
         const uint32_t hi01 = f32x2_to_bf16x2(e0, e1), hi23 = f32x2_to_bf16x2(e2, e3);
-        const uint32_t lo01 = f32x2_to_bf16x2(e0 - bf16_lo_to_f32(hi01), e1 - bf16_hi_to_f32(hi01));
-        const uint32_t lo23 = f32x2_to_bf16x2(e2 - bf16_lo_to_f32(hi23), e3 - bf16_hi_to_f32(hi23));
+        const float r0 = e0 - bf16_lo_to_f32(hi01), r1 = e1 - bf16_hi_to_f32(hi01);
+        const float r2 = e2 - bf16_lo_to_f32(hi23), r3 = e3 - bf16_hi_to_f32(hi23);
+        const uint32_t lo01 = f32x2_to_bf16x2(r0, r1), lo23 = f32x2_to_bf16x2(r2, r3);
+        if (p.fine) {
+          bt0 = movmatrix_trans(f32x2_to_bf16x2(r0 - bf16_lo_to_f32(lo01), r1 - bf16_hi_to_f32(lo01)));
+          bt1 = movmatrix_trans(f32x2_to_bf16x2(r2 - bf16_lo_to_f32(lo23), r3 - bf16_hi_to_f32(lo23)));
+        }
         bh0 = movmatrix_trans(hi01), bh1 = movmatrix_trans(hi23);
         bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
       } else {
@@ -718,9 +741,10 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       // ---- O^T += V^T P^T; only a tile with masked positions pays for the masks
       const uint32_t vrow = kFp8V ? k_row : v_row, vunit = kFp8V ? k_unit : v_unit;
       if (boundary)
-        pv_tile<kFp8V, D, true>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, vmask01, vmask89);
+        pv_tile<kFp8V, D, true>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, p.fine, bt0, bt1, vmask01,
+                                vmask89);
       else
-        pv_tile<kFp8V, D, false>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, 0u, 0u);
+        pv_tile<kFp8V, D, false>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, p.fine, bt0, bt1, 0u, 0u);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[stage]);
@@ -1043,7 +1067,8 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   // workspace holds fewer pieces per sequence than that needs.
   const uint64_t max_tiles = (uint64_t(a.max_blocks_per_seq) * a.block_size + kTile - 1) / kTile;
   const uint64_t fixed = kHeaderBytes + count_bytes(a.num_seqs, a.num_kv_heads);
-  p.max_chunk_tiles = a.max_chunk_tiles;
+  p.max_chunk_tiles = a.fine ? kSumTiles : UINT32_MAX;
+  p.fine = a.fine;
   p.max_splits = 0;
   p.min_chunk_tiles = 0;
   if (a.workspace && a.workspace_bytes > fixed && max_tiles > 1) {

@@ -127,7 +127,7 @@ struct DecodeArgs {
   const float* v_scales;  // place of k_scale and v_scale
   void* workspace;
   size_t workspace_bytes;
-  uint32_t max_chunk_tiles;  // split-KV: most 16-position tiles summed in one piece
+  bool fine;  // shorter sums and finer weights (decode.cu)
 };
 
 size_t decode_workspace_bytes(uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_q_heads,

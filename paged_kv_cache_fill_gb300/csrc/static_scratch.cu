@@ -109,6 +109,6 @@ extern "C" int paged_decode_attn_fp8k_static_scratch(
   a.fp8 = true;
   a.workspace = scratch;
   a.workspace_bytes = kStaticScratchBytes;
-  a.max_chunk_tiles = UINT32_MAX;
+  a.fine = false;
   return launch_decode(a, static_cast<cudaStream_t>(stream));
 }
