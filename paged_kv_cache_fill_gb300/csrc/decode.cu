@@ -84,6 +84,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 //     (error 2^-26 instead of 2^-17): on 64 sequences under a window of 1,000 and
 //     four sinks 2.2e-6 -> 1.2e-6 in the same 47 us.
 constexpr uint32_t kSumTiles = 192;
+// Tables of at most kWholeTiles tiles are not split by these calls: no combine
+// to launch (FP8 block scales, 8 heads of 128, us whole / split: 2 sequences of
+// 100 10.3 / 12.6, of 128 11.0 / 11.5, of 192 14.8 / 11.6; 200 sequences of 100
+// 13.8 / 19.0).
+constexpr uint32_t kWholeTiles = 8;
 
 enum : int32_t {
   kFirst = 1,    // first tile of an item
@@ -1079,7 +1084,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
       c = kMinChunkTiles;
     else if (fit >= 2)
       c = (max_tiles - 2) / (fit - 1) + 1;  // the least c with max_pieces(max_tiles, c) <= fit
-    if (c) {
+    if (c && !(a.fine && max_tiles <= kWholeTiles)) {
       p.min_chunk_tiles = uint32_t(c);
       p.max_splits = uint32_t(max_pieces(max_tiles, c));
       uint8_t* ws = static_cast<uint8_t*>(a.workspace);
