@@ -161,7 +161,8 @@ __device__ __forceinline__ float pow2_scale(uint32_t amax) {
 }
 
 template <int D, int W, bool kVec>
-__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) block_write_kernel(const __grid_constant__ BlockWriteParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm)
+    block_write_kernel(const __grid_constant__ BlockWriteParams p) {
   constexpr uint32_t kLanes = D / 8;            // lanes per row
   constexpr uint32_t kStep = W * (32 / kLanes);  // rows that the task's warps load at a time
   extern __shared__ uint4 s_data[];              // [stage][load][thread]
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) block_write_kernel(co
     if (i < p.steps_per_cta) fetch(step_of(i), 0, stage(i));
     cp_async_commit();
   }
+  uint32_t turn = 0;  // of s_max: flipped at every barrier, not at every step (steps with nothing to write have none)
   for (uint32_t i = 0; i < p.steps_per_cta; ++i) {
     if (i + kStages - 1 < p.steps_per_cta) fetch(step_of(i + kStages - 1), 0, stage(i + kStages - 1));
     cp_async_commit();
@@ -258,10 +260,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) block_write_kernel(co
     uint32_t m = largest(std::false_type{});
     if (m >= 0x7f80u) m = largest(std::true_type{});  // (the same in every lane) some value is not finite
     if constexpr (W > 1) {
-      if (lane == 0) s_max[i & 1][warp] = m;  // (not over maxima that a slower warp has yet to read)
-      __syncthreads();                        // (also: every warp of the task has read the present scale)
+      if (lane == 0) s_max[turn][warp] = m;  // (not over maxima that a slower warp has yet to read)
+      __syncthreads();                       // (also: every warp of the task has read the present scale)
 #pragma unroll
-      for (uint32_t w = 0; w < W; ++w) m = max(m, s_max[i & 1][warp / W * W + w]);
+      for (uint32_t w = 0; w < W; ++w) m = max(m, s_max[turn][warp / W * W + w]);
+      turn ^= 1;
     } else {
       __syncwarp();
     }

@@ -187,6 +187,26 @@ def test_write_block_many_sequences_and_streams():
     cache.check()
 
 
+@pytest.mark.parametrize("D,bs,H", [(128, 64, 1), (128, 128, 1), (64, 256, 3), (256, 32, 1)])
+def test_write_block_steps_with_nothing_to_write(D, bs, H):
+    """2,000 sequences of a token or two, so that items with nothing to write stand between those of one CTA, by tasks
+    of several warps, with scales that differ from block to block: no warp may take another step's maximum."""
+    rng = np.random.default_rng(D + bs)
+    B = 2000
+    new = rng.integers(0, 3, B)
+    lens = np.maximum(new, rng.integers(1, bs + 8, B))
+    tables, nb = permuted_tables(rng, lens, bs)
+    cache = Cache(nb, bs, H, D, scale=2.0 ** -20)
+    for c in cache.codes:
+        c[:] = rng.integers(0, 127, c.shape)
+    cache.upload()
+    T = int(new.sum())
+    size = 2.0 ** rng.integers(-30, 31, (T, H, 1))
+    key, value = (bf16((rng.standard_normal((T, H, D)) * size).reshape(T, H * D)) for _ in range(2))
+    write_both(cache, key, value, tables, lens, np.concatenate([[0], np.cumsum(new)]), H, D, bs)
+    cache.check()
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
