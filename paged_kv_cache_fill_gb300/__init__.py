@@ -408,6 +408,8 @@ def kv_copy_blocks(pools, src_blocks, dst_blocks, num_pairs, num_blocks, stream=
     """Copy block src_blocks[i] to dst_blocks[i] in every one of `pools`, a
     sequence of tensors of num_blocks blocks each (every layer's caches and
     scales). Pairs with a negative id are padding."""
+    if isinstance(pools, torch.Tensor):
+        raise TypeError("pools is a sequence of tensors (a tensor alone would be taken apart into its blocks)")
     dev = _device()
     for t in pools:  # (as _ptr does, which would cost a call per pool: a model has hundreds)
         if not isinstance(t, torch.Tensor):
@@ -421,7 +423,8 @@ def kv_copy_blocks(pools, src_blocks, dst_blocks, num_pairs, num_blocks, stream=
             raise ValueError(f"pool {i} does not hold {num_blocks} equal blocks")
     sizes = array.array("Q", [size // num_blocks for size in sizes])
     _check("kv_copy_blocks", lib().kv_copy_blocks(
-        bases.buffer_info()[0], sizes.buffer_info()[0], len(bases), _ptr(src_blocks), _ptr(dst_blocks), num_pairs, num_blocks, _stream(stream)))
+        bases.buffer_info()[0], sizes.buffer_info()[0], len(bases), _ptr(src_blocks), _ptr(dst_blocks), num_pairs,
+        num_blocks, _stream(stream)))
 
 
 def kv_free_blocks(block_tables, ref_counts, first_block, end_block, max_blocks_per_seq, num_seqs, num_blocks,

@@ -153,6 +153,13 @@ def test_reference_e4m3_is_the_format():
     assert ref.e4m3_codes(np.array([1e9, -1e9, np.inf, np.nan])).tolist() == [0x7E, 0xFE, 0x7E, 0x7F]
 
 
+def test_copy_refuses_one_tensor_as_the_pools(pk):
+    """Taken as a sequence, a pool would be copied as num_blocks pools of a block each."""
+    ids = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(TypeError, match="sequence"):
+        pk.kv_copy_blocks(torch.zeros(4, 4, 64, dtype=torch.uint8), ids, ids, 1, 4)
+
+
 def test_reference_scale_is_least():
     for amax in (448.0, 448.0001, 1.0, 3e38, 2.0 ** -60, 0.0, 1.75 * 2.0 ** -40, 1.7500001 * 2.0 ** -40):
         s = ref.pow2_scale(amax)
