@@ -195,7 +195,8 @@ static int decode_common(const kv_bf16_t* q, const void* k_cache, const void* v_
                          uint32_t num_seqs, uint32_t num_q_heads, uint32_t num_kv_heads, uint32_t head_dim,
                          uint32_t block_size, float inv_sqrt_d, float k_scale, uint32_t q_stride,
                          uint32_t sliding_window, bool fp8, bool fp8_v, float v_scale, bool fine,
-                         uint32_t num_sinks, bool block_scales, const float* k_scales, const float* v_scales, void* stream) {
+                         uint32_t num_sinks, bool block_scales, const float* k_scales, const float* v_scales,
+                         void* stream) {
   if (num_seqs == 0) return KV_OK;
   if (!q || !k_cache || !v_cache || !output || !block_tables || !seq_lens) return KV_ERR_INVALID_ARG;
   if (block_scales && (!k_scales || !v_scales)) return KV_ERR_INVALID_ARG;

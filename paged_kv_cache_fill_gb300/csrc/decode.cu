@@ -202,9 +202,9 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t head_base, uint32_t row, 
 // -------------------------------------------------------------- O^T += V^T P^T
 // One 16-token tile of the PV product for one warp: acc[i] holds the 16-dim
 // block i of O^T (8 query-head columns). B fragments (bh*, bl*) are the hi and
-// lo parts of P^T, bt* (with `three`, BF16 V) what they leave; kMask zeroes the V values of masked positions (their rows
-// may hold NaN), with vmask01 / vmask89 covering this lane's tokens 2c4, 2c4+1
-// and 2c4+8, 2c4+9.
+// lo parts of P^T, bt* (with `three`, BF16 V) what they leave; kMask zeroes
+// the V values of masked positions (their rows may hold NaN), with vmask01 /
+// vmask89 covering this lane's tokens 2c4, 2c4+1 and 2c4+8, 2c4+9.
 //   BF16 V: per 16-dim block one transposing ldmatrix (rows: 16 tokens).
 //   FP8 V: one transposing ldmatrix covers 32 dims x 16 tokens: matrix m holds
 //     tokens 8(m&1).. of 16-byte unit 2(jj&3)+(m>>1) and gives this lane the

@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
-    const Item it = locate<kTc2Rows>(blockIdx.x, p, lane, reinterpret_cast<uint32_t*>(smem));  // (free until the Q rows)
+    // (shared memory that is free until the Q rows)
+    const Item it = locate<kTc2Rows>(blockIdx.x, p, lane, reinterpret_cast<uint32_t*>(smem));
     if (lane == 0) s_item = it;
   }
   if (warp == 1) tmem_alloc(&tmem_base_s, Lay::kTmemCols);
@@ -827,7 +828,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
     float rs = p.score_scale;
     {
       constexpr uint32_t kLanes = D / 8, kPer = 32 / kLanes;  // lanes per row, rows per load
-      const int64_t off = valid ? int64_t(uint64_t(it.qstart + tok) * p.q_stride + uint64_t(it.kv_head * g + hh) * D) : -1;
+      const int64_t off =
+          valid ? int64_t(uint64_t(it.qstart + tok) * p.q_stride + uint64_t(it.kv_head * g + hh) * D) : -1;
       uint8_t* qt = smem + Lay::kQ0 + t * Lay::kQBytes;
       const uint32_t u = lane % kLanes;  // the 16-byte unit of the row
       uint4 qv[kLanes];
@@ -958,7 +960,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
 #pragma unroll
           for (int g2 = 0; g2 < int(kGroups); ++g2) {
             const float* xg = x + kSub * g2;
-            const float a = fmax3(fmax3(xg[0], xg[1], xg[2]), xg[3], xg[4]), b = fmax3(fmax3(xg[5], xg[6], xg[7]), xg[8], xg[9]);
+            const float a = fmax3(fmax3(xg[0], xg[1], xg[2]), xg[3], xg[4]);
+            const float b = fmax3(fmax3(xg[5], xg[6], xg[7]), xg[8], xg[9]);
             const float c = fmax3(fmax3(xg[10], xg[11], xg[12]), xg[13], xg[14]);
             gm[g2] = fmaf(fmax3(fmaxf(a, xg[15]), b, c) * rs, ks[g2], vl[g2]);
           }
@@ -1109,7 +1112,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 h[q] = f32x2_to_bf16x2(__uint_as_float(ov[k + 2 * q]) * inv, __uint_as_float(ov[k + 2 * q + 1]) * inv);
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(stage) + c0 + k) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(stage) + c0 + k) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
             }
           } else {
 #pragma unroll
