@@ -73,17 +73,17 @@ constexpr int kMinChunkTiles = 4;    // smallest chunk: 64 positions
 constexpr int kSplitUnitTiles = 16;  // the workspace-size formula's split unit: 256 positions
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The calls with sinks or block scales hold their 32-bit results to a few
-// 2^-20 (`fine`), where the earlier calls, whose bits stay as they were, do not:
+// The calls with sinks or block scales hold their 32-bit results to 2^-20
+// (kFine), where the earlier calls, whose bits stay as they were, do not:
 //   - The tensor cores add to an accumulator towards zero, so the error of a sum
-//     grows with its length. Under split-KV one accumulator sums at most
-//     kSumTiles tiles: on 64 sequences of 32,768 positions (FP8, 8 heads of 128) a
-//     CTA's whole share of 431 tiles is 7.8e-6 of the result off and takes 637 us,
-//     pieces of at most 192 tiles are 2.9e-6 off and take 646 (128: 2.0e-6, 651).
+//     grows with its length. A tile's products go into accumulators of their
+//     own, added to the running ones to nearest: on 64 sequences of 32,768
+//     positions (FP8 block scales, 8 heads of 128; 431 tiles to a sum) 7.8e-6
+//     -> 1.1e-6 of the result for 641 -> 645 us. (Sums cut at 192 tiles into
+//     more partials instead: 2.9e-6, 648 us.)
 //   - With a BF16 V the weights enter as three BF16 parts instead of two
-//     (error 2^-26 instead of 2^-17): on 64 sequences under a window of 1,000 and
-//     four sinks 2.2e-6 -> 1.2e-6 in the same 47 us.
-constexpr uint32_t kSumTiles = 192;
+//     (error 2^-26 instead of 2^-17): with the above, on 64 sequences under a
+//     window of 1,000 and four sinks, 2.2e-6 -> 2.1e-7 in the same 48 us.
 // Tables of at most kWholeTiles tiles are not split by these calls: no combine
 // to launch (FP8 block scales, 8 heads of 128, us whole / split: 2 sequences of
 // 100 10.3 / 12.6, of 128 11.0 / 11.5, of 192 14.8 / 11.6; 200 sequences of 100
@@ -120,8 +120,6 @@ struct DecodeParams {
   const float* v_scales;
   uint32_t max_splits;  // 0: no workspace, one item per (sequence, head group)
   uint32_t min_chunk_tiles;  // chunks at least this long keep every sequence within max_splits pieces
-  uint32_t max_chunk_tiles;  // longest chunk (min_chunk_tiles permitting)
-  uint32_t fine;             // BF16 V: weights in three parts
   float score_scale;    // inv_sqrt_d * log2(e)   (times k_scale for FP8)
   float out_scale;      // FP8 V: v_scale / 2^8 (P enters the MMA scaled by 2^8)
   uint32_t stages, stage_bytes, k_bytes, v_bytes;  // shared-memory ring geometry
@@ -199,10 +197,16 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t head_base, uint32_t row, 
   }
 }
 
+__device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
+  const float2 x = f2_split(f2_add(f2_make(a[0], a[1]), f2_make(b[0], b[1])));
+  const float2 y = f2_split(f2_add(f2_make(a[2], a[3]), f2_make(b[2], b[3])));
+  a[0] = x.x, a[1] = x.y, a[2] = y.x, a[3] = y.y;
+}
+
 // -------------------------------------------------------------- O^T += V^T P^T
 // One 16-token tile of the PV product for one warp: acc[i] holds the 16-dim
 // block i of O^T (8 query-head columns). B fragments (bh*, bl*) are the hi and
-// lo parts of P^T, bt* (with `three`, BF16 V) what they leave; kMask zeroes
+// lo parts of P^T, bt* (kFine, BF16 V) what they leave; kMask zeroes
 // the V values of masked positions (their rows may hold NaN), with vmask01 /
 // vmask89 covering this lane's tokens 2c4, 2c4+1 and 2c4+8, 2c4+9.
 //   BF16 V: per 16-dim block one transposing ldmatrix (rows: 16 tokens).
@@ -212,30 +216,55 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t head_base, uint32_t row, 
 //     permutation regroups them by dim and each pair converts exactly to f16.
 //     A-row g8 is dim 2g8 and A-row g8+8 dim 2g8+1 of the 16-dim block, so
 //     the accumulator rows come out in that order too.
-template <bool kFp8V, int D, bool kMask>
+template <bool kFp8V, bool kFine, int D, bool kMask>
 __device__ __forceinline__ void pv_tile(float (&acc)[D / 16][4], uint32_t vbase, uint32_t row, uint32_t unit_lo,
-                                        uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1, bool three,
+                                        uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1,
                                         uint32_t bt0, uint32_t bt1, uint32_t vmask01, uint32_t vmask89) {
   constexpr int kVRow = D * (kFp8V ? 1 : 2);  // bytes of one head's V row
   if constexpr (!kFp8V) {
-    uint32_t a[D / 16][4];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      ldmatrix_x4_trans(a[i], tile_addr<kVRow>(vbase, row, 2 * i + unit_lo));
+    auto load = [&](uint32_t (&a)[4], int i) {
+      ldmatrix_x4_trans(a, tile_addr<kVRow>(vbase, row, 2 * i + unit_lo));
       if constexpr (kMask) {
-        a[i][0] &= vmask01;
-        a[i][1] &= vmask01;
-        a[i][2] &= vmask89;
-        a[i][3] &= vmask89;
+        a[0] &= vmask01;
+        a[1] &= vmask01;
+        a[2] &= vmask89;
+        a[3] &= vmask89;
       }
-      mma_bf16(acc[i], a[i], bh0, bh1);
-    }
-    // the lo parts after every hi part: no MMA waits on the one before
+    };
+    // the lo parts after kN hi parts: no MMA waits on the one before (all of D 256's
+    // at a time would spill)
+    constexpr int kN = D == 64 ? 4 : 8;
+    if constexpr (kFine) {
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) mma_bf16(acc[i], a[i], bl0, bl1);
-    if (three) {
+      for (int i0 = 0; i0 < D / 16; i0 += kN) {
+        uint32_t a[kN][4];
+        float t[kN][4];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) mma_bf16(acc[i], a[i], bt0, bt1);
+        for (int i = 0; i < kN; ++i) {
+          load(a[i], i0 + i);
+          t[i][0] = t[i][1] = t[i][2] = t[i][3] = 0.0f;
+          mma_bf16(t[i], a[i], bh0, bh1);
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) mma_bf16(t[i], a[i], bl0, bl1);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) mma_bf16(t[i], a[i], bt0, bt1);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          add4(acc[i0 + i], t[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i0 = 0; i0 < D / 16; i0 += kN) {
+        uint32_t a[kN][4];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          load(a[i], i0 + i);
+          mma_bf16(acc[i0 + i], a[i], bh0, bh1);
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) mma_bf16(acc[i0 + i], a[i], bl0, bl1);
+      }
     }
   } else {
 #pragma unroll
@@ -260,10 +289,20 @@ __device__ __forceinline__ void pv_tile(float (&acc)[D / 16][4], uint32_t vbase,
         }
       }
       // hi, hi, lo, lo: no MMA waits on the accumulator of the one before
-      mma_f16(acc[2 * jj], a[0], bh0, bh1);
-      mma_f16(acc[2 * jj + 1], a[1], bh0, bh1);
-      mma_f16(acc[2 * jj], a[0], bl0, bl1);
-      mma_f16(acc[2 * jj + 1], a[1], bl0, bl1);
+      if constexpr (kFine) {
+        float t[2][4] = {};
+        mma_f16(t[0], a[0], bh0, bh1);
+        mma_f16(t[1], a[1], bh0, bh1);
+        mma_f16(t[0], a[0], bl0, bl1);
+        mma_f16(t[1], a[1], bl0, bl1);
+        add4(acc[2 * jj], t[0]);
+        add4(acc[2 * jj + 1], t[1]);
+      } else {
+        mma_f16(acc[2 * jj], a[0], bh0, bh1);
+        mma_f16(acc[2 * jj + 1], a[1], bh0, bh1);
+        mma_f16(acc[2 * jj], a[0], bl0, bl1);
+        mma_f16(acc[2 * jj + 1], a[1], bl0, bl1);
+      }
     }
   }
 }
@@ -280,7 +319,7 @@ constexpr bool two_ctas_per_sm() { return kFp8V && D <= 128 && NT == 1; }
 
 constexpr uint32_t kMaxItemHeads = 8;  // heads per item, at most (geometry)
 
-template <bool kFp8, bool kFp8V, bool kBlk, int D, int NT>
+template <bool kFp8, bool kFp8V, bool kBlk, bool kFine, int D, int NT>
 __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const DecodeParams p) {
@@ -291,6 +330,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   constexpr int kVCoord = kVRow >= 128 ? kVRow / 128 : 1;
   static_assert(kFp8 || !kFp8V, "an FP8 V cache comes with an FP8 K cache");
   static_assert(kFp8V || !kBlk, "block scales come with an FP8 K and V cache");
+  static_assert(kFine || !kBlk, "the call with block scales takes sinks too");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -299,7 +339,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   StageMeta* meta = reinterpret_cast<StageMeta*>(empty + p.stages);
   // kBlk: a stage's K scales of the item's heads, then its V scales
   float* scales = reinterpret_cast<float*>(meta + p.stages);
-  __shared__ uint64_t s_chunk, s_total, s_per_cta;
+  __shared__ uint64_t s_chunk, s_total;
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t num_consumers = p.heads_per_item * NT;
@@ -315,9 +355,8 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   }
   __syncthreads();
 
-  // Chunk size: the stream's tiles over the CTAs, cut once more into equal
-  // chunks of at most max_chunk_tiles, never below the minimum chunk (or the
-  // larger one a small workspace imposes).
+  // Chunk size: the stream's tiles over the CTAs, never below the minimum
+  // chunk (or the larger one a small workspace imposes).
   if (p.max_splits > 0) {
     uint64_t local = 0;
     for (uint32_t s = threadIdx.x; s < p.num_seqs; s += blockDim.x)
@@ -329,9 +368,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
     if (threadIdx.x == 0) {
       s_total *= p.num_head_groups;
       const uint64_t share = (s_total + gridDim.x - 1) / gridDim.x;
-      s_per_cta = share > p.max_chunk_tiles ? (share + p.max_chunk_tiles - 1) / p.max_chunk_tiles : 1;
-      const uint64_t want = (share + s_per_cta - 1) / s_per_cta;
-      s_chunk = want > p.min_chunk_tiles ? want : p.min_chunk_tiles;
+      s_chunk = share > p.min_chunk_tiles ? share : p.min_chunk_tiles;
     }
     __syncthreads();
   }
@@ -440,40 +477,35 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
     };
 
     if (p.max_splits > 0) {
-      // Stream-K: chunk k holds stream tiles [k C, (k + 1) C), and CTA b takes
-      // chunks b n .. b n + n - 1 (n = s_per_cta), so the walker only moves
-      // forward. The piece of (sequence, head group) range [a, b) that lies in
+      // Stream-K: chunk k holds stream tiles [k C, (k + 1) C); CTA b takes
+      // chunk b. The piece of (sequence, head group) range [a, b) that lies in
       // chunk k is its piece k - floor(a / C).
       const uint64_t C = s_chunk, total = s_total;
-      const uint64_t nchunks = (total + C - 1) / C;
       Walker wk;
       wk.chunk_base = 0;
       wk.load(0, p, lane);
-      const uint64_t k1 = (uint64_t(blockIdx.x) + 1) * s_per_cta;
-      for (uint64_t k = uint64_t(blockIdx.x) * s_per_cta; ok && k < k1 && k < nchunks; ++k) {
-        uint64_t g = k * C;
-        const uint64_t g1 = g + C < total ? g + C : total;
-        while (ok && g < g1) {
-          while (wk.chunk_seq < p.num_seqs && g >= wk.chunk_base + wk.chunk_total) {
-            wk.chunk_base += wk.chunk_total;
-            wk.load(wk.chunk_seq + 32, p, lane);
-          }
-          if (wk.chunk_seq >= p.num_seqs) break;  // not reached: g < total
-          const uint64_t rel = g - wk.chunk_base;
-          const uint32_t sl = __ffs(__ballot_sync(0xffffffffu, wk.incl > rel)) - 1;
-          const uint32_t s = wk.chunk_seq + sl;
-          const SeqSpan span = seq_span(__shfl_sync(0xffffffffu, wk.raw_len, sl), p);
-          const uint64_t nt = uint64_t(span.ntiles);  // > 0: the ballot skips empty sequences
-          const uint64_t seq_base = wk.chunk_base + __shfl_sync(0xffffffffu, wk.incl, sl) - nt * p.num_head_groups;
-          const uint32_t hg = uint32_t((g - seq_base) / nt);
-          const uint64_t a = seq_base + uint64_t(hg) * nt, b = a + nt;
-          const uint64_t e = b < g1 ? b : g1;
-          const uint32_t split = uint32_t(k - a / C);
-          // the piece that ends the pair records how many pieces it has
-          if (e == b && lane == 0) p.ws_count[uint64_t(s) * p.num_head_groups + hg] = split + 1;
-          emit(s, hg, split, span, int32_t(g - a), int32_t(e - a), (g == a && e == b) ? kSingle : 0);
-          g = e;
+      uint64_t g = blockIdx.x * C;
+      const uint64_t g1 = g + C < total ? g + C : total;
+      while (ok && g < g1) {
+        while (wk.chunk_seq < p.num_seqs && g >= wk.chunk_base + wk.chunk_total) {
+          wk.chunk_base += wk.chunk_total;
+          wk.load(wk.chunk_seq + 32, p, lane);
         }
+        if (wk.chunk_seq >= p.num_seqs) break;  // not reached: g < total
+        const uint64_t rel = g - wk.chunk_base;
+        const uint32_t sl = __ffs(__ballot_sync(0xffffffffu, wk.incl > rel)) - 1;
+        const uint32_t s = wk.chunk_seq + sl;
+        const SeqSpan span = seq_span(__shfl_sync(0xffffffffu, wk.raw_len, sl), p);
+        const uint64_t nt = uint64_t(span.ntiles);  // > 0: the ballot skips empty sequences
+        const uint64_t seq_base = wk.chunk_base + __shfl_sync(0xffffffffu, wk.incl, sl) - nt * p.num_head_groups;
+        const uint32_t hg = uint32_t((g - seq_base) / nt);
+        const uint64_t a = seq_base + uint64_t(hg) * nt, b = a + nt;
+        const uint64_t e = b < g1 ? b : g1;
+        const uint32_t split = uint32_t(blockIdx.x - a / C);
+        // the piece that ends the pair records how many pieces it has
+        if (e == b && lane == 0) p.ws_count[uint64_t(s) * p.num_head_groups + hg] = split + 1;
+        emit(s, hg, split, span, int32_t(g - a), int32_t(e - a), (g == a && e == b) ? kSingle : 0);
+        g = e;
       }
     } else {
       // no workspace: whole (sequence, head group) items, statically strided
@@ -653,8 +685,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       s[3] *= hs1;
       // ---- mask positions outside [start, len) and the sinks
       const int32_t p0 = mt.tile * kTile;
-      const bool boundary = (p0 < mt.start && p0 + kTile > p.num_sinks) || p0 + kTile > mt.len;
-      auto attended = [&](int32_t pos) { return (pos >= mt.start || pos < p.num_sinks) && pos < mt.len; };
+      const int32_t sinks = kFine ? p.num_sinks : 0;
+      const bool boundary = (p0 < mt.start && p0 + kTile > sinks) || p0 + kTile > mt.len;
+      auto attended = [&](int32_t pos) { return (pos >= mt.start || pos < sinks) && pos < mt.len; };
       if (boundary) {
         const int32_t pa = p0 + int32_t(g8), pb = pa + 8;
         if (!attended(pa)) s[0] = s[1] = -INFINITY;
@@ -718,7 +751,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         const float r0 = e0 - bf16_lo_to_f32(hi01), r1 = e1 - bf16_hi_to_f32(hi01);
         const float r2 = e2 - bf16_lo_to_f32(hi23), r3 = e3 - bf16_hi_to_f32(hi23);
         const uint32_t lo01 = f32x2_to_bf16x2(r0, r1), lo23 = f32x2_to_bf16x2(r2, r3);
-        if (p.fine) {
+        if constexpr (kFine) {
           bt0 = movmatrix_trans(f32x2_to_bf16x2(r0 - bf16_lo_to_f32(lo01), r1 - bf16_hi_to_f32(lo01)));
           bt1 = movmatrix_trans(f32x2_to_bf16x2(r2 - bf16_lo_to_f32(lo23), r3 - bf16_hi_to_f32(lo23)));
         }
@@ -746,10 +779,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       // ---- O^T += V^T P^T; only a tile with masked positions pays for the masks
       const uint32_t vrow = kFp8V ? k_row : v_row, vunit = kFp8V ? k_unit : v_unit;
       if (boundary)
-        pv_tile<kFp8V, D, true>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, p.fine, bt0, bt1, vmask01,
-                                vmask89);
+        pv_tile<kFp8V, kFine, D, true>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, bt0, bt1, vmask01, vmask89);
       else
-        pv_tile<kFp8V, D, false>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, p.fine, bt0, bt1, 0u, 0u);
+        pv_tile<kFp8V, kFine, D, false>(acc, vbase, vrow, vunit, bh0, bh1, bl0, bl1, bt0, bt1, 0u, 0u);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[stage]);
@@ -961,13 +993,13 @@ Geometry geometry(bool fp8, bool fp8_v, uint32_t head_dim, uint32_t num_kv_heads
   return g;
 }
 
-template <bool kFp8, bool kFp8V, bool kBlk, int D, int NT>
+template <bool kFp8, bool kFp8V, bool kBlk, bool kFine, int D, int NT>
 int launch_decode_t(const DecodeArgs& a, cudaStream_t stream, const Geometry& geo, DecodeParams& p) {
   CUtensorMap mk, mv;
   if (!encode_pool_map(&mk, a.k_cache, kFp8, a.num_kv_heads, D, geo.heads_per_item) ||
       !encode_pool_map(&mv, a.v_cache, kFp8V, a.num_kv_heads, D, geo.heads_per_item))
     return KV_ERR_CUDA;
-  auto kern = decode_kernel<kFp8, kFp8V, kBlk, D, NT>;
+  auto kern = decode_kernel<kFp8, kFp8V, kBlk, kFine, D, NT>;
   // The dynamic shared-memory opt-in is set once per device and size (so
   // that calls made while a stream is being captured into a CUDA graph after
   // a first eager call issue no attribute change).
@@ -1072,8 +1104,6 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   // workspace holds fewer pieces per sequence than that needs.
   const uint64_t max_tiles = (uint64_t(a.max_blocks_per_seq) * a.block_size + kTile - 1) / kTile;
   const uint64_t fixed = kHeaderBytes + count_bytes(a.num_seqs, a.num_kv_heads);
-  p.max_chunk_tiles = a.fine ? kSumTiles : UINT32_MAX;
-  p.fine = a.fine;
   p.max_splits = 0;
   p.min_chunk_tiles = 0;
   if (a.workspace && a.workspace_bytes > fixed && max_tiles > 1) {
@@ -1094,32 +1124,51 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     }
   }
 
-  const int key = (a.k_scales ? 300 : fp8_v ? 200 : a.fp8 ? 100 : 0) + int(a.head_dim / 64) * 10 + int(geo.nt);
+  const int key = (a.fine ? 1000 : 0) + (a.k_scales ? 300 : fp8_v ? 200 : a.fp8 ? 100 : 0) +
+                  int(a.head_dim / 64) * 10 + int(geo.nt);
   switch (key) {
-    case 11: return launch_decode_t<false, false, false, 64, 1>(a, stream, geo, p);
-    case 12: return launch_decode_t<false, false, false, 64, 2>(a, stream, geo, p);
-    case 21: return launch_decode_t<false, false, false, 128, 1>(a, stream, geo, p);
-    case 22: return launch_decode_t<false, false, false, 128, 2>(a, stream, geo, p);
-    case 41: return launch_decode_t<false, false, false, 256, 1>(a, stream, geo, p);
-    case 42: return launch_decode_t<false, false, false, 256, 2>(a, stream, geo, p);
-    case 111: return launch_decode_t<true, false, false, 64, 1>(a, stream, geo, p);
-    case 112: return launch_decode_t<true, false, false, 64, 2>(a, stream, geo, p);
-    case 121: return launch_decode_t<true, false, false, 128, 1>(a, stream, geo, p);
-    case 122: return launch_decode_t<true, false, false, 128, 2>(a, stream, geo, p);
-    case 141: return launch_decode_t<true, false, false, 256, 1>(a, stream, geo, p);
-    case 142: return launch_decode_t<true, false, false, 256, 2>(a, stream, geo, p);
-    case 211: return launch_decode_t<true, true, false, 64, 1>(a, stream, geo, p);
-    case 212: return launch_decode_t<true, true, false, 64, 2>(a, stream, geo, p);
-    case 221: return launch_decode_t<true, true, false, 128, 1>(a, stream, geo, p);
-    case 222: return launch_decode_t<true, true, false, 128, 2>(a, stream, geo, p);
-    case 241: return launch_decode_t<true, true, false, 256, 1>(a, stream, geo, p);
-    case 242: return launch_decode_t<true, true, false, 256, 2>(a, stream, geo, p);
-    case 311: return launch_decode_t<true, true, true, 64, 1>(a, stream, geo, p);
-    case 312: return launch_decode_t<true, true, true, 64, 2>(a, stream, geo, p);
-    case 321: return launch_decode_t<true, true, true, 128, 1>(a, stream, geo, p);
-    case 322: return launch_decode_t<true, true, true, 128, 2>(a, stream, geo, p);
-    case 341: return launch_decode_t<true, true, true, 256, 1>(a, stream, geo, p);
-    case 342: return launch_decode_t<true, true, true, 256, 2>(a, stream, geo, p);
+    case 11: return launch_decode_t<false, false, false, false, 64, 1>(a, stream, geo, p);
+    case 12: return launch_decode_t<false, false, false, false, 64, 2>(a, stream, geo, p);
+    case 21: return launch_decode_t<false, false, false, false, 128, 1>(a, stream, geo, p);
+    case 22: return launch_decode_t<false, false, false, false, 128, 2>(a, stream, geo, p);
+    case 41: return launch_decode_t<false, false, false, false, 256, 1>(a, stream, geo, p);
+    case 42: return launch_decode_t<false, false, false, false, 256, 2>(a, stream, geo, p);
+    case 111: return launch_decode_t<true, false, false, false, 64, 1>(a, stream, geo, p);
+    case 112: return launch_decode_t<true, false, false, false, 64, 2>(a, stream, geo, p);
+    case 121: return launch_decode_t<true, false, false, false, 128, 1>(a, stream, geo, p);
+    case 122: return launch_decode_t<true, false, false, false, 128, 2>(a, stream, geo, p);
+    case 141: return launch_decode_t<true, false, false, false, 256, 1>(a, stream, geo, p);
+    case 142: return launch_decode_t<true, false, false, false, 256, 2>(a, stream, geo, p);
+    case 211: return launch_decode_t<true, true, false, false, 64, 1>(a, stream, geo, p);
+    case 212: return launch_decode_t<true, true, false, false, 64, 2>(a, stream, geo, p);
+    case 221: return launch_decode_t<true, true, false, false, 128, 1>(a, stream, geo, p);
+    case 222: return launch_decode_t<true, true, false, false, 128, 2>(a, stream, geo, p);
+    case 241: return launch_decode_t<true, true, false, false, 256, 1>(a, stream, geo, p);
+    case 242: return launch_decode_t<true, true, false, false, 256, 2>(a, stream, geo, p);
+    case 1011: return launch_decode_t<false, false, false, true, 64, 1>(a, stream, geo, p);
+    case 1012: return launch_decode_t<false, false, false, true, 64, 2>(a, stream, geo, p);
+    case 1021: return launch_decode_t<false, false, false, true, 128, 1>(a, stream, geo, p);
+    case 1022: return launch_decode_t<false, false, false, true, 128, 2>(a, stream, geo, p);
+    case 1041: return launch_decode_t<false, false, false, true, 256, 1>(a, stream, geo, p);
+    case 1042: return launch_decode_t<false, false, false, true, 256, 2>(a, stream, geo, p);
+    case 1111: return launch_decode_t<true, false, false, true, 64, 1>(a, stream, geo, p);
+    case 1112: return launch_decode_t<true, false, false, true, 64, 2>(a, stream, geo, p);
+    case 1121: return launch_decode_t<true, false, false, true, 128, 1>(a, stream, geo, p);
+    case 1122: return launch_decode_t<true, false, false, true, 128, 2>(a, stream, geo, p);
+    case 1141: return launch_decode_t<true, false, false, true, 256, 1>(a, stream, geo, p);
+    case 1142: return launch_decode_t<true, false, false, true, 256, 2>(a, stream, geo, p);
+    case 1211: return launch_decode_t<true, true, false, true, 64, 1>(a, stream, geo, p);
+    case 1212: return launch_decode_t<true, true, false, true, 64, 2>(a, stream, geo, p);
+    case 1221: return launch_decode_t<true, true, false, true, 128, 1>(a, stream, geo, p);
+    case 1222: return launch_decode_t<true, true, false, true, 128, 2>(a, stream, geo, p);
+    case 1241: return launch_decode_t<true, true, false, true, 256, 1>(a, stream, geo, p);
+    case 1242: return launch_decode_t<true, true, false, true, 256, 2>(a, stream, geo, p);
+    case 1311: return launch_decode_t<true, true, true, true, 64, 1>(a, stream, geo, p);
+    case 1312: return launch_decode_t<true, true, true, true, 64, 2>(a, stream, geo, p);
+    case 1321: return launch_decode_t<true, true, true, true, 128, 1>(a, stream, geo, p);
+    case 1322: return launch_decode_t<true, true, true, true, 128, 2>(a, stream, geo, p);
+    case 1341: return launch_decode_t<true, true, true, true, 256, 1>(a, stream, geo, p);
+    case 1342: return launch_decode_t<true, true, true, true, 256, 2>(a, stream, geo, p);
     default: return KV_ERR_UNSUPPORTED;
   }
 }

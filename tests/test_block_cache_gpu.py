@@ -328,6 +328,32 @@ def test_decode_with_sinks(kind, split, D, bs, Hq, H, W, S):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_decode_sums_of_a_long_sequence(kind):
+    """30,000 positions in one sum (no workspace), V positive so that nothing cancels. 1,875 tiles are added to nearest,
+    each addition off by at most 2^-24 of a sum that grows evenly: a third of their squares on average, so 6 sigma is 6
+    sqrt(1875 / 3) 2^-24 = 9e-6 of the result. Scores: dz = (D + 8) 2^-23 |z| at most, of alternating sign over the
+    positions; with the weights' 2^-22 another 2^-19 covers them. (Additions towards zero would be 1,875 times half of
+    2^-23 times a half: 5.6e-5.)"""
+    rng = np.random.default_rng(17)
+    L, D, H, bs = 30000, 64, 1, 256
+    pool = Pool(rng, kind, [L], [1], H, D, bs, 0, 0)
+    v = pool.raw[1]
+    pool.raw[1] = v & 0x7F if v.dtype == torch.uint8 else v.abs()
+    if pool.scales:
+        pool.scales[1][:] = 2.0 ** -5                     # one scale, so that every position weighs alike
+        pool.rows[1][0] = ref.e4m3_values(pool.raw[1].cpu().numpy())[pool.tables[0, np.arange(L) // bs],
+                                                                    np.arange(L) % bs] * 2.0 ** -5
+    q = bf16(rng.standard_normal((1, 2 * D))).to(DEV)
+    out = torch.full((1, 2, D), float("nan"), device=DEV)
+    pk.kv_set_decode_workspace(None)
+    call(pool, "decode", q, out, [L], None, 2, 0, 0)
+    want = np.stack([ref.attention(f64(q).reshape(2, D)[h], pool.rows[0][0][:, 0], np.abs(pool.rows[1][0][:, 0]), L - 1, 0,
+                                   0, D ** -0.5)[0] for h in range(2)])
+    err = np.linalg.norm(f64(out)[0] - want) / np.linalg.norm(want)
+    assert err <= 9e-6 + 2.0 ** -19, err
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("D,bs,Hq,H,W,S", [(64, 16, 4, 2, 0, 4), (128, 16, 8, 2, 5, 1), (128, 32, 6, 2, 100, 17),
                                            (128, 64, 3, 3, 33, 200), (64, 16, 16, 1, 1, 0), (64, 128, 5, 1, 20, 129),
                                            (128, 16, 4, 1, 130, 64)])
@@ -376,8 +402,9 @@ def test_sinks_change_nothing_without_a_window(kind):
     """num_sinks without a window, and a window with no sinks, give the plain calls' values. The prefill's bits where
     there is no window (BF16 rows: their rounding); with one it begins its key tiles elsewhere, so that both are within
     the weights' rounding of the same value (2 max|v| 2^-11 each, and the sums' 2^-18), `out` rounded to BF16 besides.
-    The decode's bits over an E4M3 V; over a BF16 V the plain call's weights have 16 bits (2 max|v| 2^-17, and the
-    sums' 2^-18)."""
+    The decode adds its tiles to nearest, the plain one towards zero: 2 products for each of 19 tiles, each cut by at most
+    2^-23 of a sum that is on average half of max|v| times the weights' sum, 2^-18.75 in all. The weights have 22 bits over
+    an E4M3 V (each side 2 max|v| 2^-22), over a BF16 V the plain call's have 16 (2 max|v| 2^-17)."""
     rng = np.random.default_rng(4)
     lens, new = np.array([300, 17]), np.array([50, 17])
     pool = Pool(rng, kind, lens, new, 2, 128, 16, 0, 0)
@@ -404,10 +431,8 @@ def test_sinks_change_nothing_without_a_window(kind):
         one = torch.empty((2, 4, 128), device=DEV)
         call(pool, "decode", q[:2], one, lens, None, 4, W, 0)
         vmax = max(np.abs(v).max() for v in pool.rows[1])
-        if kind == "fp8":
-            assert torch.equal(dec, one)
-        else:
-            assert float((dec - one).abs().max()) <= 2 * vmax * (2.0 ** -17 + 2.0 ** -18)
+        weights = 2 * 2.0 ** -22 if kind == "fp8" else 2.0 ** -17
+        assert float((dec - one).abs().max()) <= 2 * vmax * (weights + 2.0 ** -18)
         if W == 0:
             assert torch.equal(pre.to(torch.bfloat16), out)
         else:
