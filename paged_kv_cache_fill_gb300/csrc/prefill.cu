@@ -314,12 +314,14 @@ constexpr float kRescaleLog2 = 8.0f;  // reference-max slack of the online softm
 //     warp 0      TMA producer of 128-key K tiles, warp 2 of V tiles, each a
 //                 2-stage ring whose stage is free once the MMA thread's
 //                 commit after its last reader has arrived on its empty
-//                 barrier; with an E4M3 V cache warp 2 converts each V
-//                 tile into its f16 stage before it loads the next: at
+//                 barrier; with an E4M3 V cache warp 2 converts V tiles
+//                 into their f16 stages, each before it loads the next (at
+//                 head_dim 128 without block scales the second half of a
+//                 tile's keys, with them none: kSoftKeys): at
 //                 head_dim 128 in place, the tile loaded into the upper
 //                 half of its f16 stage (E4M3 row r lies where the f16
-//                 tile's second chunk puts row r, and a lane reads the
-//                 whole row before it writes), at head_dim 64 from a ring
+//                 tile's second chunk puts row r, and a row is read
+//                 before it is written), at head_dim 64 from a ring
 //                 of its own;
 //     warp 1      owns TMEM (all 512 columns) and issues every tcgen05.mma;
 //     warp 3      with an E4M3 K cache: turns each E4M3 K tile, loaded by
@@ -335,7 +337,8 @@ constexpr float kRescaleLog2 = 8.0f;  // reference-max slack of the online softm
 //     their P of tile j, off the path of that tile's PV product (each
 //     warpgroup half of it with an E4M3 K cache; with a BF16 K cache a
 //     quarter each, warp 3 the other half: one warp converting a whole
-//     tile per cycle became the serial path). At the end each thread stages its O / l row in the
+//     tile per cycle became the serial path), or their keys of an E4M3 one
+//     (kSoftKeys). At the end each thread stages its O / l row in the
 //     then free Q tiles and K/V stages and stores it with one bulk copy
 //     (direct stores of a row per thread wrote 16 bytes per 32-byte sector
 //     and took ~3 us per CTA).
@@ -400,6 +403,14 @@ __global__ void __launch_bounds__(32 * 12, 1)
   static_assert(kFp8V || !kBlk, "block scales come with an E4M3 K and V cache");
   using Lay = Tc2Layout<D, kFp8, kFp8V>;
   constexpr uint32_t kChunks = Lay::kChunks;
+  // E4M3 V: the keys of a tile that the softmax warps convert, half of them
+  // each; warp 2 the rest, and until it has it does not load the next tile. At
+  // head_dim 128 warp 2 alone was the longest loop (us, keys 0 / 64 / 128: 8
+  // chunks of 1,024 at 4,096 to 8,192 with block scales 667 / 652 / 634; without,
+  // 8 of 512 at 4,000 131 / 123 / 126, 16 of 1,500 under a window of 1,000
+  // 214 / 215 / 218); at 64 it was not (98 / - / 102).
+  constexpr uint32_t kSoftKeys = !kFp8V || Lay::kV8Ring ? 0 : kBlk ? kTcBN : kTcBN / 2;
+  constexpr bool kSelfConverts = kFp8V && kSoftKeys < kTcBN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -419,9 +430,10 @@ __global__ void __launch_bounds__(32 * 12, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTcStages; ++s) {
       mbar_init(&k_full[s], kFp8 ? 32 : 1);  // E4M3 K: the converter warp's arrivals
-      // once the tile is f16: E4M3 V, warp 2's lanes; BF16 V, the eight
-      // softmax warps (and warp 3 with a BF16 K cache)
-      mbar_init(&v_full[s], kFp8V ? 32 : (kFp8 ? 8 : 9));
+      // once the tile is f16: E4M3 V, warp 2's lanes and the eight softmax warps,
+      // where they convert; BF16 V, the eight softmax warps (and warp 3 with a
+      // BF16 K cache)
+      mbar_init(&v_full[s], kFp8V ? (kSelfConverts ? 32 : 0) + (kSoftKeys ? 8 : 0) : (kFp8 ? 8 : 9));
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_empty[s], 1);
       mbar_init(&k8_full[s], 1);
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
     // ------------------------------------------------------------ producers
     const bool is_k = warp == 0;
     const bool e4m3 = is_k ? kFp8 : kFp8V;  // this tensor's cache holds E4M3 codes
-    const bool self_converts = kFp8V && !is_k;
+    const bool self_converts = kSelfConverts && !is_k;
     const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
     uint64_t* full = is_k ? (kFp8 ? k8_full : k_full) : v8_full;  // V: converted before v_full
     uint64_t* empty = is_k ? (kFp8 ? k8_empty : k_empty) : v_empty;
@@ -496,7 +508,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
         e4m3_tile_to_f16<D>(smem + Lay::kV80 + sj * Lay::kV8Bytes, vt, live, dead0, dead1, lane);
       } else {
 #pragma unroll 1
-        for (uint32_t r = lane; r < uint32_t(kTcBN); r += 32) {
+        for (uint32_t r = kSoftKeys + lane; r < uint32_t(kTcBN); r += 32) {
           uint8_t* row1 = vt + kTcBN * 128 + r * 128;  // the E4M3 row, and the f16 tile's chunk 1 row r
           uint4 w[8];
 #pragma unroll
@@ -919,12 +931,58 @@ __global__ void __launch_bounds__(32 * 12, 1)
         if (lane == 0) mbar_arrive(&v_full[sj]);
         return true;
       };
+      // E4M3 V tile j -> f16 (exact) in place at head_dim 128, this warpgroup's
+      // keys (the codes of row r lie where the f16 tile's second chunk puts row r,
+      // so a warp has all of its rows' codes in registers before it stores). A
+      // lane takes units u and 4 + u of a row; the rows of a quarter-warp are
+      // paired (r, r ^ 5) so that neither loads nor stores meet in a bank.
+      [[maybe_unused]] auto convert_e4m3 = [&](int32_t j, uint32_t h) -> bool {
+        constexpr uint32_t kRows = kSoftKeys ? kSoftKeys / 64 : 1;  // per lane
+        const uint32_t sj = uint32_t(j) % kTcStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&v8_full[sj], uint32_t(j / kTcStages) & 1))) return false;
+        const int32_t kb = key_base_of(j), live = k_hi - kb, dead0 = dead_lo - kb, dead1 = k_lo - kb;
+        const uint32_t q8 = lane >> 2, u = lane & 3;
+        const uint32_t r0 = (4 * h + (warp & 3)) * 8 * kRows + ((q8 >> 1) ^ ((q8 & 1) * 5));
+        uint8_t* row0 = smem + Lay::kStage0 + sj * Lay::kStageBytes + Lay::kKBytes + r0 * 128;  // of chunk 0
+        uint4 w[kRows][2];
+#pragma unroll
+        for (uint32_t i = 0; i < kRows; ++i) {
+          const int32_t r = int32_t(r0 + 8 * i);
+          const bool dead = r >= live || (r >= dead0 && r < dead1);
+#pragma unroll
+          for (uint32_t c = 0; c < 2; ++c) {
+            w[i][c] = *reinterpret_cast<const uint4*>(row0 + 1024 * i + kTcBN * 128 + (((4 * c + u) ^ (r0 & 7)) << 4));
+            if (dead) w[i][c] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < kRows; ++i) {
+#pragma unroll
+          for (uint32_t c = 0; c < 2; ++c) {  // dims 64 c + 16 u ..: chunk c, units 2 u and 2 u + 1
+            const uint32_t ws[4] = {w[i][c].x, w[i][c].y, w[i][c].z, w[i][c].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              f[2 * q] = e4m3x2_to_f16x2(uint16_t(ws[q]));
+              f[2 * q + 1] = e4m3x2_to_f16x2(uint16_t(ws[q] >> 16));
+            }
+            uint8_t* drow = row0 + 1024 * i + c * (kTcBN * 128);
+            *reinterpret_cast<uint4*>(drow + (((2 * u) ^ (r0 & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4*>(drow + (((2 * u + 1) ^ (r0 & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[sj]);
+        return true;
+      };
       auto convert_v = [&](int32_t j) -> bool {
-        if constexpr (kFp8V) return true;  // E4M3 V: converted by the V producer warp
+        if constexpr (kFp8V && !kSoftKeys) return true;  // converted by the V producer warp
         const uint32_t h1 = two ? t + 1 : 2u;
 #pragma unroll 1
         for (uint32_t h = two ? t : 0u; h < h1; ++h)
-          if (!convert_v_half(j, h)) return false;
+          if (!(kFp8V ? convert_e4m3(j, h) : convert_v_half(j, h))) return false;
         return true;
       };
       float m_run = -INFINITY, l_run = 0.0f;
