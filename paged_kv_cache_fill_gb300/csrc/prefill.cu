@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
   __shared__ uint64_t s_full[2], p_full[2][2], o_full[2];  // per Q tile (P: and half of the keys)
   __shared__ uint64_t q_full, mma_done;
   __shared__ uint64_t sc_full[kBlk ? kScaleSlots : 1];  // kBlk: a tile's scales are in their slot
-  __shared__ __align__(16) float sc_k[kBlk ? kScaleSlots : 1][kGroups], sc_v[kBlk ? kScaleSlots : 1][kGroups],
-      sc_vinv[kBlk ? kScaleSlots : 1][kGroups];  // ks, log2 vs, 1 / vs
+  __shared__ __align__(16) float2 sc_kv[kBlk ? kScaleSlots : 1][kGroups];   // ks, log2 vs
+  __shared__ __align__(16) float sc_vinv[kBlk ? kScaleSlots : 1][kGroups];  // 1 / vs
   __shared__ uint32_t tmem_base_s;
   __shared__ Item s_item;
 
@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
             const uint32_t vb = __float_as_uint(vs_next);
             // the exponent, and log2 of the fraction in [1, 2): exact for powers of two
             const float man = __uint_as_float((vb & 0x007fffffu) | 0x3f800000u);
-            sc_k[sl][lane] = ks_next;
-            sc_v[sl][lane] = float(int32_t((vb >> 23) & 255u) - 127) + (man == 1.0f ? 0.0f : log2f(man));
+            const float lv = float(int32_t((vb >> 23) & 255u) - 127) + (man == 1.0f ? 0.0f : log2f(man));
+            sc_kv[sl][lane] = make_float2(ks_next, lv);
             sc_vinv[sl][lane] = 1.0f / vs_next;
             mbar_arrive(&sc_full[sl]);
           }
@@ -988,6 +988,18 @@ __global__ void __launch_bounds__(32 * 12, 1)
       float m_run = -INFINITY, l_run = 0.0f;
       bool ok = T == 0 || convert_v(0);
       for (int32_t j = 0; j < T && ok; ++j) {
+        // kBlk: the groups' scales (score scale included), while S is on its way
+        [[maybe_unused]] float ka[kGroups], vl[kGroups];
+        if constexpr (kBlk) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[uint32_t(j) % kScaleSlots], uint32_t(j / kScaleSlots) & 1));
+          if (!ok) break;
+#pragma unroll
+          for (int g2 = 0; g2 < int(kGroups); ++g2) {
+            const float2 kv = sc_kv[uint32_t(j) % kScaleSlots][g2];
+            ka[g2] = rs * kv.x;
+            vl[g2] = kv.y;
+          }
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], uint32_t(j) & 1));
         if (!ok) break;
         tc_fence_after();
@@ -1010,10 +1022,6 @@ __global__ void __launch_bounds__(32 * 12, 1)
         if constexpr (kBlk) {
           // per group of 16 keys: the largest score times the group's scale,
           // plus log2 of its V scale
-          ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[uint32_t(j) % kScaleSlots], uint32_t(j / kScaleSlots) & 1));
-          if (!ok) break;
-          const float* ks = sc_k[uint32_t(j) % kScaleSlots];
-          const float* vl = sc_v[uint32_t(j) % kScaleSlots];
           float gm[kGroups];
 #pragma unroll
           for (int g2 = 0; g2 < int(kGroups); ++g2) {
@@ -1021,7 +1029,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
             const float a = fmax3(fmax3(xg[0], xg[1], xg[2]), xg[3], xg[4]);
             const float b = fmax3(fmax3(xg[5], xg[6], xg[7]), xg[8], xg[9]);
             const float c = fmax3(fmax3(xg[10], xg[11], xg[12]), xg[13], xg[14]);
-            gm[g2] = fmaf(fmax3(fmaxf(a, xg[15]), b, c) * rs, ks[g2], vl[g2]);
+            gm[g2] = fmaf(fmax3(fmaxf(a, xg[15]), b, c), ka[g2], vl[g2]);
           }
           tile_max = fmax3(fmax3(gm[0], gm[1], gm[2]), fmax3(gm[3], gm[4], gm[5]), fmaxf(gm[6], gm[7]));
         } else {
@@ -1073,27 +1081,24 @@ __global__ void __launch_bounds__(32 * 12, 1)
         // time (the V rows of keys at or past k_hi were zeroed as the tile
         // was converted)
         if constexpr (kBlk) {
-          const float* ks = sc_k[uint32_t(j) % kScaleSlots];
-          const float* vl = sc_v[uint32_t(j) % kScaleSlots];
-          const float* vi = sc_vinv[uint32_t(j) % kScaleSlots];
+          F2 l2 = 0ull;
 #pragma unroll
           for (int c = 0; c < kTcBN / 32; ++c) {
             uint32_t pw[16];
 #pragma unroll
             for (int g2 = 0; g2 < 2; ++g2) {
-              const float a = rs * ks[2 * c + g2], b = vl[2 * c + g2] - mbp;
-              const F2 sc2 = f2_make(a, a), add2 = f2_make(b, b);
-              F2 sum2[2] = {0ull, 0ull};
+              const float vi = sc_vinv[uint32_t(j) % kScaleSlots][2 * c + g2], b = vl[2 * c + g2] - mbp;
+              const F2 sc2 = f2_make(ka[2 * c + g2], ka[2 * c + g2]), add2 = f2_make(b, b);
+              F2 sum2 = 0ull;
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
                 const int k = 16 * c + 8 * g2 + q;
                 const float2 e = f2_split(f2_fma(f2_make(x[2 * k], x[2 * k + 1]), sc2, add2));
                 const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-                sum2[q & 1] = f2_add(sum2[q & 1], f2_make(e0, e1));
+                sum2 = q == 0 ? f2_make(e0, e1) : f2_add(sum2, f2_make(e0, e1));
                 pw[8 * g2 + q] = f32x2_to_f16x2(e0, e1);
               }
-              const float2 s01 = f2_split(f2_add(sum2[0], sum2[1]));
-              sum = fmaf(s01.x + s01.y, vi[2 * c + g2], sum);
+              l2 = f2_fma(sum2, f2_make(vi, vi), l2);
             }
             tmem_st16(scol + 16 * c, pw);
             if (c == 1) {
@@ -1102,6 +1107,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
               mbar_arrive(&p_full[t][0]);
             }
           }
+          const float2 l01 = f2_split(l2);
+          sum = l01.x + l01.y;
         } else {
           const F2 sc2 = f2_make(rs, rs), nmb2 = f2_make(-mbp, -mbp);
           F2 sum2[4] = {0ull, 0ull, 0ull, 0ull};
