@@ -148,7 +148,7 @@ def _check(name: str, status: int) -> None:
 # The smallest calls are bound by this module, not by their kernels, so a tensor
 # that passes costs four short calls into torch; what is wrong with one that
 # does not is found out afterwards (a 9-tensor call: 20 us of host time with a
-# torch.cuda.current_device() per tensor and a Stream object, 10 us like this).
+# torch.cuda.current_device() per tensor and a Stream object, 11 us like this).
 _device = torch._C._cuda_getDevice
 
 
