@@ -874,6 +874,10 @@ __global__ void __launch_bounds__(32 * 12, 1)
         *reinterpret_cast<uint4*>(qt + (u >> 3) * (kTcBM * 128) + r2 * 128 + (((u & 7) ^ (r2 & 7)) << 4)) = qv[i];
       }
     }
+    // a scale that underflows (queries near the smallest numbers) would make NaN of
+    // a masked score, -inf (the calls with sinks take positive scales only)
+    constexpr float kLeast = 1.17549435e-38f;
+    if (p.bf16_out) rs = fmaxf(rs, kLeast);
     fence_async_smem();
     mbar_arrive(&q_full);
     if (t == 1 && !two) {
@@ -996,7 +1000,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
 #pragma unroll
           for (int g2 = 0; g2 < int(kGroups); ++g2) {
             const float2 kv = sc_kv[uint32_t(j) % kScaleSlots][g2];
-            ka[g2] = rs * kv.x;
+            ka[g2] = fmaxf(rs * kv.x, kLeast);
             vl[g2] = kv.y;
           }
         }

@@ -385,6 +385,27 @@ def test_block_scales_of_any_size(form):
     check_rows(pool, form, q, out, lens, new, 4, 0, 0)
 
 
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_queries_near_the_smallest_numbers(kind, form):
+    """Queries of 2^-120 (and least K scales): every score is 0 but for 2^-100, the masked ones among them."""
+    rng = np.random.default_rng(12)
+    lens, new = np.array([200, 64, 300]), np.array([1, 1, 1]) if form == "decode" else np.array([40, 64, 5])
+    pool = Pool(rng, kind, lens, new, 2, 128, 16, 30, 4)
+    if pool.scales:
+        live = np.isfinite(pool.scales[0])
+        for s, L in enumerate(lens):                      # the reference's keys at the new scale
+            blk = pool.tables[s, np.arange(L) // 16]
+            old = np.where(live[blk], pool.scales[0][blk], 1.0).astype(np.float64)
+            pool.rows[0][s] = pool.rows[0][s] / old[..., None] * 2.0 ** -60
+        pool.scales[0][live] = 2.0 ** -60
+    T = int(new.sum())
+    q = bf16(rng.standard_normal((T, 4 * 128)) * 2.0 ** -120).to(DEV)
+    out = torch.empty((T, 4, 128), device=DEV, dtype=torch.float32 if form == "decode" else torch.bfloat16)
+    call(pool, form, q, out, lens, np.concatenate([[0], np.cumsum(new)]), 4, 30, 4)
+    check_rows(pool, form, q, out, lens, new, 4, 30, 4)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_queries_before_the_first_position_give_zeros(kind):
     rng = np.random.default_rng(3)
