@@ -832,11 +832,14 @@ __global__ void __launch_bounds__(32 * 12, 1)
     // The warp's 32 Q rows into the tile's shared-memory tile ([chunk][row][128
     // B], 128-byte swizzled), zeros past the item. D / 8 lanes take a row
     // together, so that a load covers whole rows (a row per thread, 32 rows'
-    // 16-byte pieces to a load, took 5.5 us of an item's first 9 us). E4M3 K cache:
-    // the row as f16, times 2^e with e chosen so that its largest magnitude
-    // lies in [2^14, 2^15) (exact for BF16 values in range; e at most 126, so
-    // that 2^e and 2^-e stay normal for subnormal rows), and the row's score
-    // scale rs undoes 2^e.
+    // 16-byte pieces to a load, took 5.5 us of an item's first 9 us). BF16 K cache:
+    // by asynchronous copies from a loop that is not unrolled, since a CTA runs this
+    // once and fetching the code is most of its time (unrolled, through
+    // registers: 4.2 us of an item, so 2.0). E4M3 K cache: through registers
+    // (the loop below takes longer from shared memory), the row as f16, times 2^e
+    // with e chosen so that its largest magnitude lies in [2^14, 2^15) (exact for
+    // BF16 values in range; e at most 126, so that 2^e and 2^-e stay normal for
+    // subnormal rows), and the row's score scale rs undoes 2^e.
     float rs = p.score_scale;
     {
       constexpr uint32_t kLanes = D / 8, kPer = 32 / kLanes;  // lanes per row, rows per load
@@ -844,16 +847,29 @@ __global__ void __launch_bounds__(32 * 12, 1)
           valid ? int64_t(uint64_t(it.qstart + tok) * p.q_stride + uint64_t(it.kv_head * g + hh) * D) : -1;
       uint8_t* qt = smem + Lay::kQ0 + t * Lay::kQBytes;
       const uint32_t u = lane % kLanes;  // the 16-byte unit of the row
-      uint4 qv[kLanes];
+      // unit u of row i kPer + lane / kLanes: chunk u / 8, unit u % 8 of its 128-byte row
+      auto slot = [&](uint32_t i) {
+        const uint32_t r2 = (warp & 3) * 32 + i * kPer + lane / kLanes;
+        return reinterpret_cast<uint4*>(qt + (u >> 3) * (kTcBM * 128) + r2 * 128 + (((u & 7) ^ (r2 & 7)) << 4));
+      };
+      auto source = [&](uint32_t i) { return __shfl_sync(0xffffffffu, off, i * kPer + lane / kLanes); };
+      if constexpr (!kFp8) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < kLanes; ++i) {
+          const int64_t o = source(i);
+          cp_async16_or_zeros(slot(i), p.q + (o >= 0 ? o + 8 * u : 0), o >= 0);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+      } else {
+        uint4 qv[kLanes];
 #pragma unroll
-      for (uint32_t i = 0; i < kLanes; ++i) {
-        const int64_t o = __shfl_sync(0xffffffffu, off, i * kPer + lane / kLanes);
-        qv[i] = o >= 0 ? *reinterpret_cast<const uint4*>(p.q + o + 8 * u) : make_uint4(0, 0, 0, 0);
-      }
+        for (uint32_t i = 0; i < kLanes; ++i) {
+          const int64_t o = source(i);
+          qv[i] = o >= 0 ? *reinterpret_cast<const uint4*>(p.q + o + 8 * u) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-      for (uint32_t i = 0; i < kLanes; ++i) {
-        const uint32_t r2 = (warp & 3) * 32 + i * kPer + lane / kLanes;  // the row of this lane's unit
-        if constexpr (kFp8) {
+        for (uint32_t i = 0; i < kLanes; ++i) {
           // the largest |q| of the row as a BF16 pattern
           uint32_t m = __vmaxu2(__vmaxu2(qv[i].x & 0x7fff7fffu, qv[i].y & 0x7fff7fffu),
                                 __vmaxu2(qv[i].z & 0x7fff7fffu, qv[i].w & 0x7fff7fffu));
@@ -866,12 +882,10 @@ __global__ void __launch_bounds__(32 * 12, 1)
           uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) w4[q] = f32x2_to_f16x2(bf16_lo_to_f32(w4[q]) * sc, bf16_hi_to_f32(w4[q]) * sc);
-          qv[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          *slot(i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           const int32_t mine = __shfl_sync(0xffffffffu, e, (lane % kPer) * kLanes);
           if (lane / kPer == i) rs = p.score_scale * __uint_as_float(uint32_t(127 - mine) << 23);
         }
-        // 16-byte unit u: chunk u / 8, unit u % 8 of its 128-byte row
-        *reinterpret_cast<uint4*>(qt + (u >> 3) * (kTcBM * 128) + r2 * 128 + (((u & 7) ^ (r2 & 7)) << 4)) = qv[i];
       }
     }
     // a scale that underflows (queries near the smallest numbers) would make NaN of
