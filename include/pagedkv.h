@@ -421,8 +421,9 @@ PAGEDKV_API int paged_prefill_attn_fp8_sinks(const kv_bf16_t *q, const kv_e4m3_t
  *        +-448
  *   where s' exceeds the present scale, the earlier positions' codes c become
  *        E4M3(c * scale / s'): exact unless that is below 2^-6
- * A block that holds no earlier position takes its scale from the new values
- * alone, whatever its entry held. Rows of the block past seq_lens[s] stay as
+ * Present scales are powers of two, as this call writes them. A block that
+ * holds no earlier position takes its scale from the new values alone, whatever
+ * its entry held. Rows of the block past seq_lens[s] stay as
  * they are. A block may not be written for two sequences in one call (copy a
  * shared one first: kv_fork_blocks, kv_copy_blocks). A negative table entry
  * skips its positions, and positions below 0 or past the table are skipped. A
@@ -468,8 +469,9 @@ PAGEDKV_API int paged_prefill_attn_fp8_block(const kv_bf16_t *q, const kv_e4m3_t
  * Pages of a cache (not on the pages): copying, sharing on a fork, freeing and
  * compacting, all on device-resident block tables, with no host round trip.
  * ref_counts int32[num_blocks] holds the number of table entries that name
- * each block; a block whose count is 0 (or less) is free. Allocation takes the free blocks
- * with the lowest ids, so every result is a function of the inputs alone. Ids
+ * each block; a block whose count is 0 (or less) is free. Allocation takes the
+ * free blocks with the lowest ids, so every result is a function of the inputs
+ * alone. Ids
  * and rows are checked against num_blocks and num_seqs on the device: one out of
  * range is skipped and sets bit 4 of the fault word. The calls on one set of
  * tables and counts belong on one stream, or in an order of the caller's.
