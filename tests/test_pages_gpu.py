@@ -314,3 +314,59 @@ def test_the_calls_together():
     t.copy_(nt)
     assert torch.equal(decode(qd), before)
     assert pk.kv_get_device_error() == 0
+
+
+def test_page_calls_in_a_captured_graph():
+    """A fork with its page copy, a release and a compaction with its copy captured once (on a stream of its own),
+    replayed over three other states that are put into the same buffers."""
+    rng = np.random.default_rng(31)
+    B, width, nb, bs, forks, size = 40, 9, 400, 16, 12, 4096
+    t, lens, refs = (torch.zeros(s, dtype=torch.int32, device=DEV) for s in ((B, width), (B,), (nb,)))
+    src, dst, first, end = (torch.zeros(n, dtype=torch.int32, device=DEV) for n in (forks, forks, B, B))
+    cs, cd = (torch.zeros(forks, dtype=torch.int32, device=DEV) for _ in range(2))
+    nt, nr, ids, num = torch.zeros_like(t), torch.zeros_like(refs), torch.zeros_like(refs), torch.zeros_like(refs[:1])
+    ms, md = (torch.zeros(nb // 2, dtype=torch.int32, device=DEV) for _ in range(2))
+    pools = [torch.zeros((nb, n), dtype=torch.uint8, device=DEV) for n in (size, 32)]
+
+    def run():
+        pk.kv_fork_blocks(t, lens, refs, src, dst, cs, cd, forks, width, B, nb, bs)
+        pk.kv_copy_blocks(pools, cs, cd, forks, nb)
+        pk.kv_free_blocks(t, refs, first, end, width, B, nb)
+        pk.kv_compact_blocks(t, refs, nt, nr, ids, ms, md, num, width, B, nb)
+        pk.kv_copy_blocks(pools, ms, md, nb // 2, nb)
+
+    run()
+    assert pk.kv_get_device_error() == BIT_RANGE           # (forks of row 0 to itself, entries of free blocks)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        ht, hl, hr = np.full((B, width), -1, np.int32), np.zeros(B, np.int32), np.zeros(nb, np.int32)
+        perm = rng.permutation(nb)
+        for s in range(20):                                # rows 20.. are free
+            hl[s] = rng.integers(0, width * bs + 1)
+            n = -(-int(hl[s]) // bs)
+            ht[s, :n], perm = perm[:n], perm[n:]
+            hr[ht[s, :n]] = 1
+        hs, hd = rng.integers(0, 20, forks).astype(np.int32), (20 + rng.permutation(20)[:forks]).astype(np.int32)
+        hf, he = np.zeros(B, np.int32), np.zeros(B, np.int32)
+        he[rng.permutation(20)[:8]] = width                # eight parents end
+        data = [rng.integers(0, 256, p.shape, dtype=np.uint8) for p in pools]
+        for dev, host in zip((t, lens, refs, src, dst, first, end, *pools), (ht, hl, hr, hs, hd, hf, he, *data)):
+            dev.copy_(torch.from_numpy(host))
+        graph.replay()
+        ws, wd = ref.fork_blocks(ht, hl, hr, hs, hd, bs)
+        for d in data:
+            d[wd[wd >= 0]] = d[ws[ws >= 0]]
+        ref.free_blocks(ht, hr, hf, he)
+        wt, wr, wi, wms, wmd, used = ref.compact_blocks(ht, hr)
+        for d in data:
+            d[wmd[wmd >= 0]] = d[wms[wms >= 0]]
+        for got, want, what in ((lens, hl, "lens"), (cs, ws, "src"), (cd, wd, "dst"), (t, ht, "tables"), (refs, hr, "refs"),
+                                (nt, wt, "new tables"), (nr, wr, "new refs"), (ids, wi, "ids"), (ms, wms, "moves"),
+                                (md, wmd, "to"), (num, [used], "used")):
+            same(got, want, what)
+        for p, d in zip(pools, data):
+            live = wr > 0                                   # (a moved block's old place is free)
+            same(p[torch.from_numpy(live).to(DEV)], d[live], "pool")
+    assert pk.kv_get_device_error() == 0
