@@ -324,7 +324,8 @@ PAGEDKV_API int paged_prefill_attn_fp8(const kv_bf16_t *q, const kv_e4m3_t *k_ca
  * first call before any stream capture, and do not call it on a device
  * after a cudaDeviceReset in the same process (the cached address belonged
  * to the reset context). All calls share the one array; no call reads what
- * an earlier one left there. Calls whose work may overlap on the GPU
+ * an earlier one left there (but for partial sums where a wait gave up: bit 0
+ * of the fault word, and that output is unspecified). Calls whose work may overlap on the GPU
  * (different streams, other devices' calls aside) race on the array: order
  * them.
  * ---------------------------------------------------------------------- */
@@ -587,7 +588,7 @@ PAGEDKV_API int kv_set_decode_workspace(void *device_ptr, size_t bytes);
  * KV_ERR_INVALID_ARG for a null bits pointer. The other calls never
  * synchronise, so they cannot see these faults and never return
  * KV_ERR_DEVICE.
- *   bit 0: a decode pipeline wait timed out
+ *   bit 0: a decode pipeline wait timed out (that call's output is unspecified)
  *   bit 1: seq_lens[s] exceeded max_blocks_per_seq * block_size (clamped)
  *   bit 2: a prefill query_start_loc was decreasing, negative or past
  *          num_q_tokens (that sequence skipped)

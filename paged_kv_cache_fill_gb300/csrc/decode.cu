@@ -486,7 +486,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       wk.load(0, p, lane);
       uint64_t g = blockIdx.x * C;
       const uint64_t g1 = g + C < total ? g + C : total;
-      while (ok && g < g1) {
+      // (after a wait that gave up the walk goes on for the piece counts alone:
+      // the combine kernel reads one for every pair)
+      while (g < g1) {
         while (wk.chunk_seq < p.num_seqs && g >= wk.chunk_base + wk.chunk_total) {
           wk.chunk_base += wk.chunk_total;
           wk.load(wk.chunk_seq + 32, p, lane);
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         const uint32_t split = uint32_t(blockIdx.x - a / C);
         // the piece that ends the pair records how many pieces it has
         if (e == b && lane == 0) p.ws_count[uint64_t(s) * p.num_head_groups + hg] = split + 1;
-        emit(s, hg, split, span, int32_t(g - a), int32_t(e - a), (g == a && e == b) ? kSingle : 0);
+        if (ok) emit(s, hg, split, span, int32_t(g - a), int32_t(e - a), (g == a && e == b) ? kSingle : 0);
         g = e;
       }
     } else {
@@ -866,7 +868,10 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
 // piece count, then each piece's (m, l) and the lane's dims of its partial
 // output, whose loads do not depend on one another. A sequence with no
 // positions has no piece in the tile stream: its output row is written as
-// zeros here.
+// zeros here. Every other pair's count is written by this call's producers,
+// also by those that gave up waiting (its partials may then be anything, as the
+// output is); the loop is held to the partials that the workspace has room for
+// all the same.
 constexpr uint32_t kCombineWarps = 8;  // per CTA
 
 template <int D>
@@ -883,14 +888,14 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Decod
     return;
   }
   const uint32_t hg = h / p.group / p.heads_per_item;
-  const int32_t nsplit = int32_t(__ldg(p.ws_count + uint64_t(s) * p.num_head_groups + hg));
+  const uint32_t nsplit = min(__ldg(p.ws_count + uint64_t(s) * p.num_head_groups + hg), p.max_splits);
   if (nsplit <= 1) return;
   const uint64_t row0 = uint64_t(s) * p.max_splits * p.num_q_heads + h;  // piece i at row0 + i * Hq
   float M = -INFINITY, den = 0.0f, acc[D / 32];
 #pragma unroll
   for (uint32_t k = 0; k < D / 32; ++k) acc[k] = 0.0f;
 #pragma unroll 4
-  for (int32_t i = 0; i < nsplit; ++i) {
+  for (uint32_t i = 0; i < nsplit; ++i) {
     const uint64_t row = row0 + uint64_t(i) * p.num_q_heads;
     const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + row * 2);
     float v[D / 32];
