@@ -503,7 +503,8 @@ PAGEDKV_API int kv_free_blocks(int32_t *block_tables, int32_t *ref_counts, const
 /* The same for the blocks that a window has left behind: those that hold
  * neither a sink nor a position at or past seq_lens[s] - sliding_window, which
  * no decode at this length or a later one, and no prefill of later tokens,
- * attends. sliding_window 0 frees nothing. */
+ * attends. sliding_window 0 frees nothing. A length past the table is cut to it,
+ * as those calls cut it, and sets bit 1. */
 PAGEDKV_API int kv_free_window_blocks(int32_t *block_tables, int32_t *ref_counts, const int32_t *seq_lens,
                                       uint32_t max_blocks_per_seq, uint32_t num_seqs, uint32_t num_blocks,
                                       uint32_t block_size, uint32_t sliding_window, uint32_t num_sinks,
@@ -597,7 +598,7 @@ PAGEDKV_API int kv_set_decode_workspace(void *device_ptr, size_t bytes);
  *   bit 4: a page call (kv_copy_blocks to kv_compact_blocks) met an id, a row
  *          or a count out of range (skipped)
  *   bit 5: kv_fork_blocks found no free block for a fork (not made)
- *   (bits 1 and 2 also cover kv_write_fp8_block; bit 0 also covers the prefill pipeline and the fused K write's wait
+ *   (bits 1 and 2 also cover kv_write_fp8_block, bit 1 kv_free_window_blocks; bit 0 also covers the prefill pipeline and the fused K write's wait
  *   for its shared-memory copy of the sin/cos table)
  * ---------------------------------------------------------------------- */
 PAGEDKV_API int kv_get_device_error(uint32_t *bits);

@@ -146,7 +146,14 @@ __global__ void __launch_bounds__(128) free_blocks_kernel(const FreeParams p) {
     b = __ldg(p.end + row);
     a = a < 0 ? 0 : a;
   } else {
-    const int64_t behind = int64_t(__ldg(p.seq_lens + row)) - p.sliding_window;  // positions below it are out of view
+    // as the attention calls cut it; positions below `behind` are out of view
+    int64_t L = __ldg(p.seq_lens + row);
+    const int64_t cap = int64_t(p.max_blocks_per_seq) * p.block_size;
+    if (L > cap) {
+      L = cap;
+      if (threadIdx.x == 0) atomicOr(&g_pages_error, kErrSeqLenClamped);
+    }
+    const int64_t behind = L - p.sliding_window;
     a = (int64_t(p.num_sinks) + p.block_size - 1) / p.block_size;
     b = behind > 0 ? behind / p.block_size : 0;
   }

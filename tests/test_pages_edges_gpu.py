@@ -1,0 +1,28 @@
+"""The page calls on states that a caller should not hand over."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_fill_gb300 as pk
+from test_pages_gpu import i32, same
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU hosts, never run there
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+@pytest.mark.parametrize("length", [65, 100, 1000, 2 ** 31 - 1])
+def test_window_release_of_a_sequence_past_its_table(length):
+    """Attention cuts such a sequence to its table's 64 positions, so what a window of 30 of those attends stays."""
+    tables = np.array([[0, 1, 2, 3], [4, 5, 6, -1]], np.int32)
+    t, r = i32(tables), i32([1] * 7)
+    pk.kv_free_window_blocks(t, r, i32([length, 40]), 4, 2, 7, 16, 30, 0)
+    same(t, [[-1, -1, 2, 3], [4, 5, 6, -1]]), same(r, [0, 0, 1, 1, 1, 1, 1])
+    assert pk.kv_get_device_error() == 2                       # as the attention calls flag it
