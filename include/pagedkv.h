@@ -456,7 +456,7 @@ PAGEDKV_API int paged_decode_attn_fp8_block(const kv_bf16_t *q, const kv_e4m3_t 
                                             void *stream);
 
 /* Multi-token form over that cache: as paged_prefill_attn_fp8_sinks (BF16
- * rows out), with the block scales. head_dim 64 or 128. */
+ * rows out), with the block scales, of the same range. head_dim 64 or 128. */
 PAGEDKV_API int paged_prefill_attn_fp8_block(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
                                              const kv_e4m3_t *v_cache_fp8, const float *k_scales,
                                              const float *v_scales, kv_bf16_t *output, const int32_t *block_tables,

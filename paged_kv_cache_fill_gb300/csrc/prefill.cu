@@ -350,12 +350,23 @@ constexpr float kRescaleLog2 = 8.0f;  // reference-max slack of the online softm
 // running maximum of z + log2 vs: the codes' products need no further scale,
 // the f16 weights keep their precision whatever the scales are, and one
 // exponential per score is enough, since the softmax sum is
-// l = sum over groups of (sum of the group's P') / vs, in the same frame.
+// l = sum over groups of (sum of the group's P') / vs, in the same frame, held as
+// 2^20 l (between 2^-93 and 2^95 for the largest key of a row, where scales are
+// from 2^-60 to 2^120).
+// Where vs is 2^kScaleSpread or more below the largest so far, P' may vanish in 32
+// bits although the key's weight in l does not. The K producer flags such groups
+// (a bit each in the slot, and 1 / vs given as 0); their scores go into a running
+// maximum and sum of their own, which join l at the end. The work for them stands in
+// the branch of the masked tiles, where it costs the others 0.5% (8 x 1,024 queries:
+// 606 -> 609 us; in a branch of its own beside the weights 617). For the same reason l
+// moves to a frame 2^126 or more above in two factors.
 // A slot is rewritten kScaleSlots tiles later: when the K producer has the K
 // stage of tile i, the softmax of tile i - 5 is done in both Q tiles (their S
 // products of tile i - 4 have run, and each follows that tile's P).
 constexpr uint32_t kScaleSlots = 8;
 constexpr uint32_t kGroups = kTcBN / kSub;  // groups of keys with one scale, per tile
+constexpr float kScaleSpread = 64.0f;       // in log2
+constexpr float kSumLog2 = 20.0f, kSumScale = 1048576.0f;  // kBlk: l is held times 2^kSumLog2
 
 constexpr int kTc2Rows = 256;
 // registers per thread of warpgroup 0 and of the softmax warpgroups after
@@ -422,7 +433,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
   __shared__ uint64_t q_full, mma_done;
   __shared__ uint64_t sc_full[kBlk ? kScaleSlots : 1];  // kBlk: a tile's scales are in their slot
   __shared__ __align__(16) float2 sc_kv[kBlk ? kScaleSlots : 1][kGroups];   // ks, log2 vs
-  __shared__ __align__(16) float sc_vinv[kBlk ? kScaleSlots : 1][kGroups];  // 1 / vs
+  __shared__ __align__(16) float sc_vinv[kBlk ? kScaleSlots : 1][kGroups];  // 2^kSumLog2 / vs
+  __shared__ uint32_t sc_far[kBlk ? kScaleSlots : 1];                       // groups far below the largest vs so far
   __shared__ uint32_t tmem_base_s;
   __shared__ Item s_item;
 
@@ -550,11 +562,13 @@ __global__ void __launch_bounds__(32 * 12, 1)
     // kBlk: this lane's group's scales, loaded a tile ahead (1 where no box is
     // loaded). A negative block id (outside the caller's contract; its box is
     // filled with zeros) takes block 0's.
-    [[maybe_unused]] float ks_next = 1.0f, vs_next = 1.0f;
+    [[maybe_unused]] float ks_next = 1.0f, vs_next = 1.0f, lv_max = -INFINITY;
+    [[maybe_unused]] bool has_next = false;
     auto load_scales = [&](int32_t i) {
       int32_t key0;
       ks_next = vs_next = 1.0f;
-      if (i < T && my_box(i, key0)) {
+      has_next = i < T && my_box(i, key0);
+      if (has_next) {
         int32_t bid = __ldg(table + (key0 >> p.block_shift));
 #ifdef PAGEDKV_DEBUG_BOUNDS
         bid = dbg_block_ok(bid) ? bid : 0;
@@ -602,14 +616,21 @@ __global__ void __launch_bounds__(32 * 12, 1)
       }
       if constexpr (kBlk) {
         if (is_k) {
+          const uint32_t sl = uint32_t(i) % kScaleSlots;
+          const uint32_t vb = __float_as_uint(vs_next);
+          // the exponent, and log2 of the fraction in [1, 2): exact for powers of two
+          const float man = __uint_as_float((vb & 0x007fffffu) | 0x3f800000u);
+          const float lv = float(int32_t((vb >> 23) & 255u) - 127) + (man == 1.0f ? 0.0f : log2f(man));
+          float top = has_next ? lv : -INFINITY;
+#pragma unroll
+          for (uint32_t o = 1; o < kGroups; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          lv_max = fmaxf(lv_max, top);  // (in the lanes of the groups)
+          const bool far = has_next && lv < lv_max - kScaleSpread;
+          const uint32_t fars = __ballot_sync(0xffffffffu, far);
           if (lane < kGroups) {
-            const uint32_t sl = uint32_t(i) % kScaleSlots;
-            const uint32_t vb = __float_as_uint(vs_next);
-            // the exponent, and log2 of the fraction in [1, 2): exact for powers of two
-            const float man = __uint_as_float((vb & 0x007fffffu) | 0x3f800000u);
-            const float lv = float(int32_t((vb >> 23) & 255u) - 127) + (man == 1.0f ? 0.0f : log2f(man));
             sc_kv[sl][lane] = make_float2(ks_next, lv);
-            sc_vinv[sl][lane] = 1.0f / vs_next;
+            sc_vinv[sl][lane] = far ? 0.0f : kSumScale / vs_next;
+            if (lane == 0) sc_far[sl] = fars;
             mbar_arrive(&sc_full[sl]);
           }
           load_scales(i + 1);
@@ -1004,10 +1025,12 @@ __global__ void __launch_bounds__(32 * 12, 1)
         return true;
       };
       float m_run = -INFINITY, l_run = 0.0f;
+      [[maybe_unused]] float far_m = -INFINITY, far_l = 0.0f;  // kBlk: largest score and sum of the groups far below
       bool ok = T == 0 || convert_v(0);
       for (int32_t j = 0; j < T && ok; ++j) {
         // kBlk: the groups' scales (score scale included), while S is on its way
         [[maybe_unused]] float ka[kGroups], vl[kGroups];
+        [[maybe_unused]] uint32_t far = 0;
         if constexpr (kBlk) {
           ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[uint32_t(j) % kScaleSlots], uint32_t(j / kScaleSlots) & 1));
           if (!ok) break;
@@ -1017,6 +1040,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
             ka[g2] = fmaxf(rs * kv.x, kLeast);
             vl[g2] = kv.y;
           }
+          far = sc_far[uint32_t(j) % kScaleSlots];
         }
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], uint32_t(j) & 1));
         if (!ok) break;
@@ -1030,11 +1054,25 @@ __global__ void __launch_bounds__(32 * 12, 1)
 #pragma unroll
         for (int k = 0; k < kTcBN; ++k) x[k] = __uint_as_float(sv[k]);
         const int32_t key_base = key_base_of(j);
-        if (key_base + kTcBN - 1 > pos || key_base < lo) {
+        if (key_base + kTcBN - 1 > pos || key_base < lo || (kBlk && far)) {
           const uint32_t off = uint32_t(key_base - p.num_sinks);
 #pragma unroll
           for (int k = 0; k < kTcBN; ++k)
             if (key_base + k > pos || off + uint32_t(k) < skipped) x[k] = -INFINITY;
+          if constexpr (kBlk) {
+            if (far) {  // (the same in every row)
+              float top = far_m;
+#pragma unroll
+              for (int k = 0; k < kTcBN; ++k)
+                if ((far >> (k / kSub)) & 1u) top = fmaxf(top, x[k] * ka[k / kSub]);
+              const float base = top == -INFINITY ? 0.0f : top;
+              far_l *= fast_exp2(far_m - base);
+              far_m = top;
+#pragma unroll
+              for (int k = 0; k < kTcBN; ++k)
+                if ((far >> (k / kSub)) & 1u) far_l += fast_exp2(fmaf(x[k], ka[k / kSub], -base));
+            }
+          }
         }
         float tile_max;
         if constexpr (kBlk) {
@@ -1072,6 +1110,10 @@ __global__ void __launch_bounds__(32 * 12, 1)
         const float al = fast_exp2(m_run - mb);
         const bool rescale = j > 0 && __any_sync(0xffffffffu, mx != m_run);
         if (rescale) {
+          if constexpr (kBlk) {
+            const float half = fast_exp2(0.5f * (m_run - mb));  // (its square may be too small)
+            l_run = l_run * half * half;
+          }
           // O changes only once PV_t(j - 1) is done
           ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], uint32_t(j - 1) & 1));
           if (!ok) break;
@@ -1151,7 +1193,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
           const float2 s01 = f2_split(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])));
           sum = s01.x + s01.y;
         }
-        l_run = l_run * al + sum;
+        l_run = kBlk ? l_run + sum : l_run * al + sum;
         m_run = mx;
         tmem_wait_st();
         tc_fence_before();
@@ -1163,7 +1205,9 @@ __global__ void __launch_bounds__(32 * 12, 1)
       // ---- O / l to the output row
       // the PV product summed E4M3 codes (v_scale dequantises them) or BF16
       // values times 2^-8
-      const float inv = l_run > 0.0f ? (kFp8V ? p.out_scale : 256.0f) / l_run : 0.0f;
+      if constexpr (kBlk)
+        if (far_l > 0.0f) l_run += far_l * fast_exp2(far_m - m_run + (kSumLog2 + 7.0f));
+      const float inv = l_run > 0.0f ? (kBlk ? kSumScale : kFp8V ? p.out_scale : 256.0f) / l_run : 0.0f;
       const uint32_t out_bytes = p.bf16_out ? D * 2 : D * 4;  // of a row
       uint8_t* o = valid ? static_cast<uint8_t*>(p.output) +
                                (uint64_t(it.qstart + tok) * p.num_q_heads + uint64_t(it.kv_head * g + hh)) * out_bytes

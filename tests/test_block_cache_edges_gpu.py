@@ -1,0 +1,58 @@
+"""The block-scaled cache and the prefills at the ends of their ranges, against the plain
+64-bit references, with the tolerances of test_block_cache_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_fill_gb300 as pk
+import reference64 as ref
+from test_block_cache_gpu import DEV, KINDS, Pool, bf16, call, check_rows, f64, i32
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU hosts, never run there
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+    yield
+    pk.kv_set_decode_workspace(None)
+
+
+def rescale(pool, i, lens, scales, zero=None):
+    """Give K (i = 0) or V (i = 1) of a block-scaled pool without a window the scales [blocks, heads], and zero codes
+    in the blocks of `zero`; the reference's rows follow."""
+    codes = pool.raw[i].cpu().numpy()
+    if zero is not None:
+        codes[zero] = 0
+    pool.raw[i] = torch.from_numpy(codes).to(DEV)
+    pool.scales[i][:] = scales
+    for s, L in enumerate(lens):
+        pos = np.arange(int(L))
+        b = pool.tables[s, pos // pool.bs]
+        pool.rows[i][s] = ref.e4m3_values(codes[b, pos % pool.bs]) * pool.scales[i][b].astype(np.float64)[..., None]
+
+
+@pytest.mark.parametrize("small", ["zero", "nonzero"])
+@pytest.mark.parametrize("high", [0, 70, 100, 117])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+def test_block_scales_far_apart(form, D, high, small):
+    """Blocks with V scales of 2^-60 (those that the write gives a block of zeros) among blocks of 2^high, in either
+    order and for rows that see one kind only: a key counts in the softmax sum whatever its V scale is."""
+    rng = np.random.default_rng(high + D)
+    lens = np.array([200, 64, 700, 16, 150])
+    new = np.ones(5, np.int64) if form == "decode" else np.array([200, 64, 30, 16, 150])
+    pool = Pool(rng, "fp8_block", lens, lens, 2, D, 16, 0, 0)
+    low = rng.random(pool.scales[1].shape[0]) < 0.5
+    low[pool.tables[0, :4]], low[pool.tables[4, :5]] = True, False       # a row's first blocks of one kind
+    rescale(pool, 1, lens, np.where(low[:, None], 2.0 ** -60, 2.0 ** high), low if small == "zero" else None)
+    T = int(new.sum())
+    q = bf16(rng.standard_normal((T, 4 * D)) * 0.3).to(DEV)
+    out = torch.empty((T, 4, D), device=DEV, dtype=torch.float32 if form == "decode" else torch.bfloat16)
+    call(pool, form, q, out, lens, np.concatenate([[0], np.cumsum(new)]), 4, 0, 0)
+    check_rows(pool, form, q, out, lens, new, 4, 0, 0)
+    assert pk.kv_get_device_error() == 0
