@@ -627,7 +627,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
             qf[kk][0] = f32x2_to_f16x2(qv[kk][0] * sc, qv[kk][1] * sc);
             qf[kk][1] = f32x2_to_f16x2(qv[kk][2] * sc, qv[kk][3] * sc);
           }
-          const float unscale = p.score_scale * ldexpf(1.0f, -e);
+          // kBlk: the score scale meets the block's K scale first (its product with 2^-e
+          // alone may lie below the normal numbers)
+          const float unscale = (kBlk ? 1.0f : p.score_scale) * ldexpf(1.0f, -e);
           head_scale[0] = __shfl_sync(0xffffffffu, unscale, (2 * c4) * 4);
           head_scale[1] = __shfl_sync(0xffffffffu, unscale, (2 * c4 + 1) * 4);
         }
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       [[maybe_unused]] float v_exp = 0.0f, v_man = 1.0f;  // kBlk: vs = 2^v_exp v_man
       if constexpr (kBlk) {
         const float* sc = scales + stage * (2 * kMaxItemHeads) + hl;
-        const float ks = sc[0];
+        const float ks = sc[0] * p.score_scale;
         const uint32_t vs = __float_as_uint(sc[kMaxItemHeads]);
         hs0 *= ks;
         hs1 *= ks;

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
   __shared__ uint64_t s_full[2], p_full[2][2], o_full[2];  // per Q tile (P: and half of the keys)
   __shared__ uint64_t q_full, mma_done;
   __shared__ uint64_t sc_full[kBlk ? kScaleSlots : 1];  // kBlk: a tile's scales are in their slot
-  __shared__ __align__(16) float2 sc_kv[kBlk ? kScaleSlots : 1][kGroups];   // ks, log2 vs
+  __shared__ __align__(16) float2 sc_kv[kBlk ? kScaleSlots : 1][kGroups];   // ks score_scale, log2 vs
   __shared__ __align__(16) float sc_vinv[kBlk ? kScaleSlots : 1][kGroups];  // 2^kSumLog2 / vs
   __shared__ uint32_t sc_far[kBlk ? kScaleSlots : 1];                       // groups far below the largest vs so far
   __shared__ uint32_t tmem_base_s;
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
           const bool far = has_next && lv < lv_max - kScaleSpread;
           const uint32_t fars = __ballot_sync(0xffffffffu, far);
           if (lane < kGroups) {
-            sc_kv[sl][lane] = make_float2(ks_next, lv);
+            sc_kv[sl][lane] = make_float2(ks_next * p.score_scale, lv);
             sc_vinv[sl][lane] = far ? 0.0f : kSumScale / vs_next;
             if (lane == 0) sc_far[sl] = fars;
             mbar_arrive(&sc_full[sl]);
@@ -861,7 +861,11 @@ __global__ void __launch_bounds__(32 * 12, 1)
     // with e chosen so that its largest magnitude lies in [2^14, 2^15) (exact for
     // BF16 values in range; e at most 126, so that 2^e and 2^-e stay normal for
     // subnormal rows), and the row's score scale rs undoes 2^e.
-    float rs = p.score_scale;
+    // With block scales rs is 2^-e alone, and the score scale comes with the K scales:
+    // its product with 2^-e may lie below the smallest number where theirs with a
+    // large K scale does not.
+    const float score_scale = kBlk ? 1.0f : p.score_scale;
+    float rs = score_scale;
     {
       constexpr uint32_t kLanes = D / 8, kPer = 32 / kLanes;  // lanes per row, rows per load
       const int64_t off =
@@ -905,14 +909,14 @@ __global__ void __launch_bounds__(32 * 12, 1)
           for (int q = 0; q < 4; ++q) w4[q] = f32x2_to_f16x2(bf16_lo_to_f32(w4[q]) * sc, bf16_hi_to_f32(w4[q]) * sc);
           *slot(i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
           const int32_t mine = __shfl_sync(0xffffffffu, e, (lane % kPer) * kLanes);
-          if (lane / kPer == i) rs = p.score_scale * __uint_as_float(uint32_t(127 - mine) << 23);
+          if (lane / kPer == i) rs = score_scale * __uint_as_float(uint32_t(127 - mine) << 23);
         }
       }
     }
     // a scale that underflows (queries near the smallest numbers) would make NaN of
     // a masked score, -inf (the calls with sinks take positive scales only)
     constexpr float kLeast = 1.17549435e-38f;
-    if (p.bf16_out) rs = fmaxf(rs, kLeast);
+    if (!kBlk && p.bf16_out) rs = fmaxf(rs, kLeast);
     fence_async_smem();
     mbar_arrive(&q_full);
     if (t == 1 && !two) {
@@ -1028,7 +1032,7 @@ __global__ void __launch_bounds__(32 * 12, 1)
       [[maybe_unused]] float far_m = -INFINITY, far_l = 0.0f;  // kBlk: largest score and sum of the groups far below
       bool ok = T == 0 || convert_v(0);
       for (int32_t j = 0; j < T && ok; ++j) {
-        // kBlk: the groups' scales (score scale included), while S is on its way
+        // kBlk: the groups' scales (the row's included), while S is on its way
         [[maybe_unused]] float ka[kGroups], vl[kGroups];
         [[maybe_unused]] uint32_t far = 0;
         if constexpr (kBlk) {

@@ -56,3 +56,26 @@ def test_block_scales_far_apart(form, D, high, small):
     call(pool, form, q, out, lens, np.concatenate([[0], np.cumsum(new)]), 4, 0, 0)
     check_rows(pool, form, q, out, lens, new, 4, 0, 0)
     assert pk.kv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("D,k_exp,q_exp,isd_exp", [(64, 110, -116, -3), (64, 120, -114, -14), (128, 120, -114, -14)])
+def test_small_queries_against_large_key_scales(form, D, k_exp, q_exp, isd_exp):
+    """Scores of a few units from queries near the smallest numbers and K scales up to the largest: the product of the
+    row's scale and the block's is in range where the row's alone is not."""
+    rng = np.random.default_rng(D - q_exp)
+    lens = np.array([200, 64, 300])
+    new = np.ones(3, np.int64) if form == "decode" else np.array([40, 64, 5])
+    pool = Pool(rng, "fp8_block", lens, lens, 2, D, 16, 0, 0)
+    rescale(pool, 0, lens, 2.0 ** k_exp)
+    T, isd = int(new.sum()), 2.0 ** isd_exp
+    q = bf16(rng.standard_normal((T, 4 * D)) * 2.0 ** q_exp).to(DEV)
+    out = torch.empty((T, 4, D), device=DEV, dtype=torch.float32 if form == "decode" else torch.bfloat16)
+    args = [q, *pool.args(), out, i32(pool.tables), i32(lens)]
+    geo = [4, 2, D, 16, isd, 4 * D, 0, 0]
+    if form == "decode":
+        pk.paged_decode_attn_fp8_block(*args, pool.tables.shape[1], 3, *geo)
+    else:
+        pk.paged_prefill_attn_fp8_block(*args, i32(np.concatenate([[0], np.cumsum(new)])), pool.tables.shape[1], 3, T, *geo)
+    # (the check's scores are scaled by D^-1/2: the rest of isd is taken into its queries)
+    check_rows(pool, form, q.double() * (isd * D ** 0.5), out, lens, new, 4, 0, 0)
