@@ -47,7 +47,9 @@
 //     < 2) enters the weights under a second running maximum M' = max(z +
 //     e): acc = sum 2^(z + e - M') m code, l = sum 2^(z - M), so that the
 //     f16 weights keep their precision whatever the scales are, and the
-//     output is acc 2^(M' - M) / l.
+//     output is acc 2^(M' - M) / l. Partials go to the workspace times
+//     kBlkPartial, since a sum of values near vs = 2^120 before the division
+//     by l may pass the largest number.
 //   * Sinks: a sequence's tile list is its sink tiles followed by its window
 //     tiles; everything else sees one list of consecutive tile numbers.
 //   * Split-KV (flash-decoding): the pieces of a sequence cut by chunk
@@ -90,6 +92,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 13.8 / 19.0).
 constexpr uint32_t kWholeTiles = 8;
 
+constexpr float kBlkPartial = 1.0f / (1 << 24);  // exact; room for sums of 2^24 positions
+
 enum : int32_t {
   kFirst = 1,    // first tile of an item
   kLast = 2,     // last tile of an item
@@ -122,6 +126,7 @@ struct DecodeParams {
   uint32_t min_chunk_tiles;  // chunks at least this long keep every sequence within max_splits pieces
   float score_scale;    // inv_sqrt_d * log2(e)   (times k_scale for FP8)
   float out_scale;      // FP8 V: v_scale / 2^8 (P enters the MMA scaled by 2^8)
+  float partial_scale;  // kBlkPartial with block scales, else 1
   uint32_t stages, stage_bytes, k_bytes, v_bytes;  // shared-memory ring geometry
 };
 
@@ -831,6 +836,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           }
         }
       } else {
+        if constexpr (kBlk) sc0 *= kBlkPartial, sc1 *= kBlkPartial;
         const uint64_t row = (uint64_t(mt.seq) * p.max_splits + mt.split) * p.num_q_heads + hq0;
         float* o0 = p.ws_o + row * D;
         float* o1 = o0 + D;
@@ -912,7 +918,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Decod
     M = Mn;
   }
 #pragma unroll
-  for (uint32_t k = 0; k < D / 32; ++k) out[lane + 32 * k] = acc[k] / den;
+  for (uint32_t k = 0; k < D / 32; ++k) out[lane + 32 * k] = acc[k] / (den * p.partial_scale);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1100,6 +1106,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.v_scales = a.v_scales;
   p.score_scale = a.inv_sqrt_d * kLog2e * (a.fp8 ? a.k_scale : 1.0f);
   p.out_scale = fp8_v ? a.v_scale * (1.0f / 256.0f) : 1.0f;
+  p.partial_scale = a.k_scales ? kBlkPartial : 1.0f;
   p.stages = geo.stages;
   p.stage_bytes = geo.stage_bytes;
   p.k_bytes = geo.k_bytes;

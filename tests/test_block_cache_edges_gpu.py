@@ -79,3 +79,22 @@ def test_small_queries_against_large_key_scales(form, D, k_exp, q_exp, isd_exp):
         pk.paged_prefill_attn_fp8_block(*args, i32(np.concatenate([[0], np.cumsum(new)])), pool.tables.shape[1], 3, T, *geo)
     # (the check's scores are scaled by D^-1/2: the rest of isd is taken into its queries)
     check_rows(pool, form, q.double() * (isd * D ** 0.5), out, lens, new, 4, 0, 0)
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_decode_of_the_largest_scale(split):
+    """V values of 2^120 and up, all positive: the sums before the division by the softmax's stay finite, in one piece
+    and in many."""
+    rng = np.random.default_rng(6)
+    lens, H, D, bs = np.array([3000, 900]), 2, 128, 16
+    pool = Pool(rng, "fp8_block", lens, lens, H, D, bs, 0, 0)
+    pool.raw[1] = torch.from_numpy(ref.e4m3_codes(rng.uniform(1, 30, tuple(pool.raw[1].shape)))).to(DEV)
+    rescale(pool, 1, lens, 2.0 ** 120)
+    ws = torch.empty(pk.kv_decode_workspace_bytes(pool.tables.shape[1], 2, 4, H, D, bs), dtype=torch.uint8,
+                     device=DEV) if split else None
+    pk.kv_set_decode_workspace(ws)
+    q = bf16(rng.standard_normal((2, 4 * D)) * 0.3).to(DEV)
+    out = torch.empty((2, 4, D), device=DEV)
+    call(pool, "decode", q, out, lens, None, 4, 0, 0)
+    check_rows(pool, "decode", q, out, lens, np.ones(2, np.int64), 4, 0, 0)
+    pk.kv_set_decode_workspace(None)
