@@ -406,10 +406,11 @@ def paged_prefill_attn_fp8_block(q, k_cache_fp8, v_cache_fp8, k_scales, v_scales
 
 def kv_copy_blocks(pools, src_blocks, dst_blocks, num_pairs, num_blocks, stream=None):
     """Copy block src_blocks[i] to dst_blocks[i] in every one of `pools`, a
-    sequence of tensors of num_blocks blocks each (every layer's caches and
-    scales). Pairs with a negative id are padding."""
+    sequence (or any iterable) of tensors of num_blocks blocks each (every
+    layer's caches and scales). Pairs with a negative id are padding."""
     if isinstance(pools, torch.Tensor):
         raise TypeError("pools is a sequence of tensors (a tensor alone would be taken apart into its blocks)")
+    pools = list(pools)  # gone through more than once
     dev = _device()
     for t in pools:  # (as _ptr does, which would cost a call per pool: a model has hundreds)
         if not isinstance(t, torch.Tensor):

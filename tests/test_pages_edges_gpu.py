@@ -1,10 +1,11 @@
-"""The page calls on states that a caller should not hand over."""
+"""The page calls on states that a caller should not hand over, and pools given as any
+iterable."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_cache_fill_gb300 as pk
-from test_pages_gpu import i32, same
+from test_pages_gpu import DEV, i32, same
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +27,11 @@ def test_window_release_of_a_sequence_past_its_table(length):
     pk.kv_free_window_blocks(t, r, i32([length, 40]), 4, 2, 7, 16, 30, 0)
     same(t, [[-1, -1, 2, 3], [4, 5, 6, -1]]), same(r, [0, 0, 1, 1, 1, 1, 1])
     assert pk.kv_get_device_error() == 2                       # as the attention calls flag it
+
+
+def test_copy_blocks_takes_pools_from_an_iterator():
+    data = torch.arange(4 * 2048, device=DEV).to(torch.uint8).view(4, 2048)
+    pools = [data.clone(), data.flip(0).contiguous()]
+    pk.kv_copy_blocks(iter(pools), i32([0]), i32([3]), 1, 4)
+    for p in pools:
+        assert torch.equal(p[3], p[0])
