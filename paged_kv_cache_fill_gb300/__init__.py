@@ -149,7 +149,9 @@ def _check(name: str, status: int) -> None:
 # that passes costs four short calls into torch; what is wrong with one that
 # does not is found out afterwards (a 9-tensor call: 20 us of host time with a
 # torch.cuda.current_device() per tensor and a Stream object, 11 us like this).
-_device = torch._C._cuda_getDevice
+# A torch built without CUDA has no such call, and without a GPU it raises: tensors
+# of the host (device -1) are refused before it is asked.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -157,7 +159,8 @@ def _ptr(t: torch.Tensor | None):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor")
-    if t.get_device() != _device() or not t.is_contiguous():
+    d = t.get_device()
+    if d < 0 or d != _device() or not t.is_contiguous():
         _refuse(t)
     return t.data_ptr() or None
 
@@ -411,11 +414,12 @@ def kv_copy_blocks(pools, src_blocks, dst_blocks, num_pairs, num_blocks, stream=
     if isinstance(pools, torch.Tensor):
         raise TypeError("pools is a sequence of tensors (a tensor alone would be taken apart into its blocks)")
     pools = list(pools)  # gone through more than once
-    dev = _device()
+    dev = _device() if torch.cuda.is_initialized() else -1
     for t in pools:  # (as _ptr does, which would cost a call per pool: a model has hundreds)
         if not isinstance(t, torch.Tensor):
             raise TypeError("expected a torch.Tensor")
-        if t.get_device() != dev or not t.is_contiguous():
+        d = t.get_device()
+        if d < 0 or d != dev or not t.is_contiguous():
             _refuse(t)
     bases = array.array("Q", [t.data_ptr() for t in pools])
     sizes = [t.nbytes for t in pools]
