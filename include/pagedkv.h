@@ -516,11 +516,11 @@ PAGEDKV_API int kv_free_window_blocks(int32_t *block_tables, int32_t *ref_counts
  * the pair (copy_src[i], copy_dst[i]) to hand to kv_copy_blocks; (-1, -1)
  * where there is none. The free blocks go to the forks in order of i. The
  * destination rows must be free (released by kv_free_blocks): what they held
- * is overwritten, not released. A row that two forks write, or that one
- * writes and another reads, makes those forks invalid: an invalid fork
- * (also: a row out of range, a length past the table) sets bit 4, one that
- * finds no free block sets bit 5; either leaves its row as it was and gets the
- * pair (-2, -2).
+ * is overwritten, not released. Forks that write the same row are invalid, and so
+ * is a fork that reads a row which a fork of this call names as its destination
+ * (the one that names it is made all the same): an invalid fork (also: a row out
+ * of range, a length past the table) sets bit 4, one that finds no free block
+ * sets bit 5; either leaves its row as it was and gets the pair (-2, -2).
  *   block_tables, seq_lens int32[num_seqs], ref_counts (16-byte aligned)
  *   updated; src_seqs, dst_seqs device int32[num_forks]; copy_src, copy_dst
  *   device int32[num_forks], written.

@@ -451,7 +451,9 @@ def kv_free_window_blocks(block_tables, ref_counts, seq_lens, max_blocks_per_seq
 def kv_fork_blocks(block_tables, seq_lens, ref_counts, src_seqs, dst_seqs, copy_src, copy_dst, num_forks,
                    max_blocks_per_seq, num_seqs, num_blocks, block_size, stream=None):
     """Make rows dst_seqs forks of rows src_seqs: full blocks shared, a partial
-    one given a free block and a (copy_src, copy_dst) pair for kv_copy_blocks."""
+    one given a free block and a (copy_src, copy_dst) pair for kv_copy_blocks.
+    Not made: forks that write one row, and a fork that reads a row which a
+    fork of the call names as its destination."""
     _check("kv_fork_blocks", lib().kv_fork_blocks(
         _ptr(block_tables), _ptr(seq_lens), _ptr(ref_counts), _ptr(src_seqs), _ptr(dst_seqs), _ptr(copy_src),
         _ptr(copy_dst), num_forks, max_blocks_per_seq, num_seqs, num_blocks, block_size, _stream(stream)))
