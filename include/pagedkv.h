@@ -478,7 +478,9 @@ PAGEDKV_API int paged_prefill_attn_fp8_block(const kv_bf16_t *q, const kv_e4m3_t
  * tables and counts belong on one stream, or in an order of the caller's.
  *
  * kv_copy_blocks: for every pool p and pair i, block dst_blocks[i] of pool p
- * becomes a copy of block src_blocks[i]. A pair with a negative id is padding.
+ * becomes a copy of block src_blocks[i]. A pair with a negative id is padding
+ * (beside a negative source the destination is not looked at; a source out of
+ * range sets bit 4 beside any destination).
  * No block may be the destination of two pairs, or of one and the source of
  * another.
  *   pools, block_bytes   HOST arrays of num_pools device base pointers and of

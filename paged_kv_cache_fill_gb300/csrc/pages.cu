@@ -67,7 +67,7 @@ __device__ __forceinline__ void copy_flat(const CopyParams& p, const CopyPool& p
   for (uint64_t e = uint64_t(blockIdx.x) * kCopyThreads + threadIdx.x; e < total;
        e += uint64_t(gridDim.x) * kCopyThreads) {
     const uint64_t pair = e / per, at = e % per;
-    const int32_t src = block_id(p, p.src[pair]), dst = block_id(p, p.dst[pair]);
+    const int32_t src = block_id(p, p.src[pair]), dst = src >= 0 ? block_id(p, p.dst[pair]) : -1;
     if (src >= 0 && dst >= 0) base[uint64_t(uint32_t(dst)) * per + at] = base[uint64_t(uint32_t(src)) * per + at];
   }
 }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_kv_cache_fill_gb300 as pk
-from test_pages_gpu import DEV, i32, same
+from test_pages_gpu import BIT_RANGE, DEV, i32, same
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,17 @@ def test_copy_blocks_takes_pools_from_an_iterator():
     pk.kv_copy_blocks(iter(pools), i32([0]), i32([3]), 1, 4)
     for p in pools:
         assert torch.equal(p[3], p[0])
+
+
+@pytest.mark.parametrize("size", [4096, 16, 12, 7])
+def test_copy_blocks_flags_the_same_pairs_in_every_way_of_copying(size):
+    """A negative source is padding, whatever its destination; a source out of range is flagged beside any."""
+    rng = np.random.default_rng(size)
+    data = torch.from_numpy(rng.integers(0, 256, (6, size), dtype=np.uint8)).to(DEV)
+    want = data.cpu().numpy().copy()
+    want[4] = want[2]
+    for src, dst, bits in (([-1, -2, 2, 3], [77, 6, 4, -1], 0), ([6, 2], [1, 4], BIT_RANGE), ([2, 2], [4, 6], BIT_RANGE),
+                           ([99, 2], [-1, 4], BIT_RANGE)):
+        pk.kv_copy_blocks([data], i32(src), i32(dst), len(src), 6)
+        same(data, want)
+        assert pk.kv_get_device_error() == bits, (src, dst)
