@@ -258,7 +258,8 @@ PAGEDKV_API int paged_decode_attn_fp8(const kv_bf16_t *q, const kv_e4m3_t *k_cac
  * [start, P] with start = (sliding_window > 0 ? max(0, P + 1 -
  * sliding_window) : 0): exactly what the paged decode attends for that
  * sequence cut to length P + 1. A query with P < 0 gives zeros. GQA,
- * inv_sqrt_d, the block tables and (FP8) k_scale are as in the decode calls.
+ * inv_sqrt_d (here >= 0), the block tables and (FP8) k_scale are as in the
+ * decode calls.
  *   q                bf16 rows [num_q_tokens], row stride q_stride elements,
  *                    head h at +h * head_dim.
  *   query_start_loc  device int32[num_seqs + 1], non-decreasing, from 0 to

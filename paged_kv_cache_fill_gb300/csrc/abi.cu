@@ -344,7 +344,8 @@ static int prefill_common(const kv_bf16_t* q, const void* k_cache, const void* v
   if (num_kv_heads == 0 || num_q_heads == 0 || num_q_heads % num_kv_heads) return KV_ERR_INVALID_ARG;
   if (head_dim == 0 || block_size == 0) return KV_ERR_INVALID_ARG;
   if (uint64_t(q_stride) < uint64_t(num_q_heads) * head_dim) return KV_ERR_INVALID_ARG;
-  if (!isfinite(inv_sqrt_d)) return KV_ERR_INVALID_ARG;
+  // (the scores' maximum is taken before the scale is applied)
+  if (!(inv_sqrt_d >= 0.0f) || !isfinite(inv_sqrt_d)) return KV_ERR_INVALID_ARG;
   if (fp8 && (!(k_scale > 0.0f) || !isfinite(k_scale))) return KV_ERR_INVALID_ARG;
   if (fp8_v && (!(v_scale > 0.0f) || !isfinite(v_scale))) return KV_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return KV_ERR_UNSUPPORTED;
@@ -420,8 +421,7 @@ int paged_prefill_attn_fp8(const kv_bf16_t* q, const kv_e4m3_t* k_cache_fp8, con
                         nullptr, stream);
 }
 
-// The scores' maximum is taken before the scale is applied, so the calls that
-// say so want a positive one.
+// The calls with sinks or block scales want a positive scale.
 static bool positive(float x) { return x > 0.0f && isfinite(x); }
 
 int paged_prefill_attn_bf16_sinks(const kv_bf16_t* q, const kv_bf16_t* k_cache, const kv_bf16_t* v_cache,
