@@ -913,10 +913,10 @@ __global__ void __launch_bounds__(32 * 12, 1)
         }
       }
     }
-    // a scale that underflows (queries near the smallest numbers) would make NaN of
-    // a masked score, -inf (the calls with sinks take positive scales only)
+    // a scale that is zero, or underflows (queries near the smallest numbers), would
+    // make NaN of a masked score, -inf (negative scales are refused)
     constexpr float kLeast = 1.17549435e-38f;
-    if (!kBlk && p.bf16_out) rs = fmaxf(rs, kLeast);
+    if (!kBlk) rs = fmaxf(rs, kLeast);
     fence_async_smem();
     mbar_arrive(&q_full);
     if (t == 1 && !two) {

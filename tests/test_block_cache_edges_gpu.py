@@ -98,3 +98,23 @@ def test_decode_of_the_largest_scale(split):
     call(pool, "decode", q, out, lens, None, 4, 0, 0)
     check_rows(pool, "decode", q, out, lens, np.ones(2, np.int64), 4, 0, 0)
     pk.kv_set_decode_workspace(None)
+
+
+@pytest.mark.parametrize("isd,q_exp,k_exp", [(None, -120, -40), (0.0, 0, None), (1e-38, 0, -20)])
+@pytest.mark.parametrize("kind", ["bf16", "fp8k", "fp8"])
+def test_prefill_of_scores_that_vanish(kind, isd, q_exp, k_exp):
+    """The prefills with float rows, where the score scale is zero or falls below the smallest number: every attended
+    position has the same weight, and a masked one has none."""
+    rng = np.random.default_rng(23)
+    lens, new, H, Hq, D, bs = np.array([200, 64, 300]), np.array([40, 64, 5]), 2, 4, 128, 16
+    pool = Pool(rng, kind, lens, new, H, D, bs, 0, 0)
+    if k_exp is not None:
+        pool.k_scale = 2.0 ** k_exp
+    T = int(new.sum())
+    q = bf16(rng.standard_normal((T, Hq * D)) * 2.0 ** q_exp).to(DEV)
+    for W in (0, 30):
+        out = torch.full((T, Hq, D), float("nan"), device=DEV)
+        getattr(pk, f"paged_prefill_attn_{kind}")(
+            q, *pool.raw, out, i32(pool.tables), i32(lens), i32(np.concatenate([[0], np.cumsum(new)])),
+            pool.tables.shape[1], 3, T, Hq, H, D, bs, D ** -0.5 if isd is None else isd, *pool.scalars(), Hq * D, W)
+        check_rows(pool, "prefill", torch.zeros_like(q), out, lens, new, Hq, W, 0)
