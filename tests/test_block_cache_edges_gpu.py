@@ -118,3 +118,22 @@ def test_prefill_of_scores_that_vanish(kind, isd, q_exp, k_exp):
             q, *pool.raw, out, i32(pool.tables), i32(lens), i32(np.concatenate([[0], np.cumsum(new)])),
             pool.tables.shape[1], 3, T, Hq, H, D, bs, D ** -0.5 if isd is None else isd, *pool.scalars(), Hq * D, W)
         check_rows(pool, "prefill", torch.zeros_like(q), out, lens, new, Hq, W, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,D,Hq,H,W,S", [(33, 64, 4, 2, 0, 0), (70, 128, 4, 1, 40, 5), (120, 64, 6, 2, 100, 17)])
+def test_prefill_of_many_sequences(kind, B, D, Hq, H, W, S):
+    """More sequences than a warp has lanes, their lengths spread over many length classes, empty ones and ones without
+    new tokens among them: every item is found by its class."""
+    rng = np.random.default_rng(B + D)
+    lens = np.exp(rng.uniform(0, np.log(1500), B)).astype(np.int64)
+    new = np.minimum(lens, rng.integers(0, 9, B))
+    lens[::11], new[::11] = 0, 0
+    new[5] = lens[5] = 300                                     # two items for each KV head
+    pool = Pool(rng, kind, lens, new, H, D, 16, W, S)
+    T = int(new.sum())
+    q = bf16(rng.standard_normal((T, Hq * D))).to(DEV)
+    out = torch.full((T, Hq, D), float("nan"), device=DEV, dtype=torch.bfloat16)
+    call(pool, "prefill", q, out, lens, np.concatenate([[0], np.cumsum(new)]), Hq, W, S)
+    check_rows(pool, "prefill", q, out, lens, new, Hq, W, S)
+    assert pk.kv_get_device_error() == 0
