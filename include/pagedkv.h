@@ -2,9 +2,11 @@
  * pagedkv.h — C ABI of the GB300 (sm_103a) paged KV-cache library.
  *
  * The paged KV-cache hot path of an LLM decode server: slot filling, cache
- * writes (BF16, FP8-E4M3 K with BF16 V, fused RMSNorm/RoPE K, V only) and
- * paged decode attention (BF16 and FP8 K). The calls and their argument
- * order follow the Rust launchers on the pages
+ * writes (BF16, FP8-E4M3 K with BF16 V, FP8 K and V, fused RMSNorm/RoPE K, V
+ * only), paged decode and chunked-prefill attention over those caches, an FP8
+ * cache with block scales, windows with sinks, and page moves. The calls that
+ * the source pages have, and their argument order, follow the Rust launchers on
+ * the pages
  *   "spark_model/layers/ops/kv_cache.rs"              (written [kv_cache.rs]) and
  *   "metrale_model_layers/layers/ops/kv_cache_fp8k.rs" (written [kv_cache_fp8k.rs]),
  * with the launcher's GPU/kernel handles dropped and the stream last.
@@ -239,7 +241,7 @@ PAGEDKV_API int paged_decode_attn_fp8k(const kv_bf16_t *q, const kv_e4m3_t *k_ca
  * argument order, with num_seqs, q_stride and sliding_window as in the
  * calls above and cache_stride dropped): as paged_decode_attn_fp8k, with
  * v_p = E4M3 code * v_scale (v_scale finite and > 0) read from a uint8 V
- * pool. Supported head_dim: {128, 256}.
+ * pool.
  * ---------------------------------------------------------------------- */
 PAGEDKV_API int paged_decode_attn_fp8(const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8,
                                       const kv_e4m3_t *v_cache_fp8, float *output, const int32_t *block_tables,
@@ -326,9 +328,9 @@ PAGEDKV_API int paged_prefill_attn_fp8(const kv_bf16_t *q, const kv_e4m3_t *k_ca
  * after a cudaDeviceReset in the same process (the cached address belonged
  * to the reset context). All calls share the one array; no call reads what
  * an earlier one left there (but for partial sums where a wait gave up: bit 0
- * of the fault word, and that output is unspecified). Calls whose work may overlap on the GPU
- * (different streams, other devices' calls aside) race on the array: order
- * them.
+ * of the fault word, and that output is unspecified). Calls whose work may
+ * overlap on the GPU (different streams, other devices' calls aside) race on
+ * the array: order them.
  * ---------------------------------------------------------------------- */
 PAGEDKV_API int paged_decode_attn_fp8k_static_scratch(
     const kv_bf16_t *q, const kv_e4m3_t *k_cache_fp8, const kv_bf16_t *v_cache, float *output,
@@ -601,8 +603,9 @@ PAGEDKV_API int kv_set_decode_workspace(void *device_ptr, size_t bytes);
  *   bit 4: a page call (kv_copy_blocks to kv_compact_blocks) met an id, a row
  *          or a count out of range (skipped)
  *   bit 5: kv_fork_blocks found no free block for a fork (not made)
- *   (bits 1 and 2 also cover kv_write_fp8_block, bit 1 kv_free_window_blocks; bit 0 also covers the prefill pipeline and the fused K write's wait
- *   for its shared-memory copy of the sin/cos table)
+ *   (bits 1 and 2 also cover kv_write_fp8_block, bit 1 kv_free_window_blocks;
+ *   bit 0 also covers the prefill pipeline and the fused K write's wait for its
+ *   shared-memory copy of the sin/cos table)
  * ---------------------------------------------------------------------- */
 PAGEDKV_API int kv_get_device_error(uint32_t *bits);
 
