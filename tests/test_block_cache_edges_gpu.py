@@ -137,3 +137,59 @@ def test_prefill_of_many_sequences(kind, B, D, Hq, H, W, S):
     call(pool, "prefill", q, out, lens, np.concatenate([[0], np.cumsum(new)]), Hq, W, S)
     check_rows(pool, "prefill", q, out, lens, new, Hq, W, S)
     assert pk.kv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("W,S", [(0, 0), (300, 20), (33, 200)])
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+def test_block_scales_drawn_over_the_whole_range(form, W, S):
+    """V scales from 2^-60 to 2^118, many not powers of two, over sequences of many tiles under windows and sinks: each
+    row is as exact as its own largest value allows."""
+    rng = np.random.default_rng(W + S + 1)
+    lens = np.array([3000, 1333, 40])
+    new = np.ones(3, np.int64) if form == "decode" else np.array([90, 7, 40])
+    pool = Pool(rng, "fp8_block", lens, new, 2, 128, 16, W, S)
+    live = np.isfinite(pool.scales[1])
+    pool.scales[1][live] = (2.0 ** rng.integers(-60, 118, int(live.sum())) * rng.choice([1.0, 1.37, 1.91], int(live.sum()))
+                            ).astype(np.float32)
+    codes = pool.raw[1].cpu().numpy()
+    for s, L in enumerate(lens):
+        pos = np.arange(int(L))
+        b = pool.tables[s, pos // 16]
+        pool.rows[1][s] = ref.e4m3_values(codes[b, pos % 16]) * pool.scales[1][b].astype(np.float64)[..., None]
+    T = int(new.sum())
+    q = bf16(rng.standard_normal((T, 4 * 128)) * rng.choice([0.3, 3.0, 20.0], (T, 1))).to(DEV)
+    ws = torch.empty(pk.kv_decode_workspace_bytes(pool.tables.shape[1], 3, 4, 2, 128, 16), dtype=torch.uint8, device=DEV)
+    for split in (False, True) if form == "decode" else (False,):
+        pk.kv_set_decode_workspace(ws if split else None)
+        out = torch.empty((T, 4, 128), device=DEV, dtype=torch.float32 if form == "decode" else torch.bfloat16)
+        call(pool, form, q, out, lens, np.concatenate([[0], np.cumsum(new)]), 4, W, S)
+        check_rows(pool, form, q, out, lens, new, 4, W, S)
+    pk.kv_set_decode_workspace(None)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill_in_a_captured_graph(kind):
+    """Captured once on a stream of its own, replayed with other queries and with the same tokens cut into other
+    sequences' chunks."""
+    rng = np.random.default_rng(29)
+    lens, Hq, H, D, bs, W, S, T = np.array([200, 64, 300]), 4, 2, 128, 16, 50, 3, 80
+    pool = Pool(rng, kind, lens, lens, H, D, bs, W, S)
+    q = torch.zeros((T, Hq * D), device=DEV, dtype=torch.bfloat16)
+    out = torch.zeros((T, Hq, D), device=DEV, dtype=torch.bfloat16)
+    tables, d_lens, d_qsl, cache = i32(pool.tables), i32(lens), i32([0, 40, 60, 80]), pool.args()
+    name = f"paged_prefill_attn_{kind}" + ("" if kind == "fp8_block" else "_sinks")
+
+    def run():
+        getattr(pk, name)(q, *cache, out, tables, d_lens, d_qsl, pool.tables.shape[1], 3, T, Hq, H, D, bs, D ** -0.5,
+                          *pool.scalars(), Hq * D, W, S)
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for new in ([40, 20, 20], [0, 64, 16], [79, 1, 0]):
+        q.copy_(bf16(rng.standard_normal((T, Hq * D))))
+        d_qsl.copy_(i32(np.concatenate([[0], np.cumsum(new)])))
+        out.fill_(float("nan"))
+        graph.replay()
+        check_rows(pool, "prefill", q, out, lens, np.array(new), Hq, W, S)
+    assert pk.kv_get_device_error() == 0
