@@ -304,10 +304,13 @@ __device__ Item locate(uint32_t target, const PrefillParams& p, uint32_t lane, u
 __device__ Item prefix_item(uint32_t target, const PrefillParams& p) {
   Item it{};
   it.seq = -1;
-  // (the piece is loaded beside what says whether it is one)
+  // (the header alone until it says that the plan is this call's: one that was made for
+  // fewer sequences or groups ends before where this call's pieces lie)
+  const uint32_t num_pieces = __ldcg(&p.plan.head->num_pieces);
+  if (!plan_fits(p.plan.head, p) || target >= num_pieces) return it;
   const int4* src = reinterpret_cast<const int4*>(p.plan.pieces + target);
   const int4 a = __ldcg(src), b = __ldcg(src + 1), c = __ldcg(src + 2);
-  if (!plan_fits(p.plan.head, p) || target >= __ldcg(&p.plan.head->num_pieces) || c.x <= 0) return it;
+  if (c.x <= 0) return it;
   it.seq = a.z;
   it.kv_head = a.w;
   it.row0 = b.x;
