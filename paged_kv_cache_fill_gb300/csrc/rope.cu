@@ -80,6 +80,19 @@ __device__ __forceinline__ void turn2(F2 x, F2 y, const PairTurn& t, F2& ox, F2&
   oy = f2_fma(y, t.cl, f2_fma(x, t.sl, f2_fma(y, t.ch, f2_mul(x, t.sh))));
 }
 
+// The same where x or y holds infinities: a pair with one takes the 16 bits alone, since its
+// products with them and with the rests may have opposite signs.
+__device__ __forceinline__ void turn2_infinite(F2 x, F2 y, const PairTurn& t, F2& ox, F2& oy) {
+  F2 fx, fy;
+  turn2(x, y, t, fx, fy);
+  const float2 x2 = f2_split(x), y2 = f2_split(y), a = f2_split(fx), b = f2_split(fy);
+  const float2 c = f2_split(f2_fma(x, t.ch, f2_mul(y, t.nsh))), d = f2_split(f2_fma(y, t.ch, f2_mul(x, t.sh)));
+  const bool fin0 = fabsf(x2.x) < INFINITY && fabsf(y2.x) < INFINITY;
+  const bool fin1 = fabsf(x2.y) < INFINITY && fabsf(y2.y) < INFINITY;
+  ox = f2_make(fin0 ? a.x : c.x, fin1 ? a.y : c.y);
+  oy = f2_make(fin0 ? b.x : d.x, fin1 ? b.y : d.y);
+}
+
 __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float scale, float recip, bool exact_div) {
   float q[4];
 #pragma unroll
@@ -263,10 +276,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid
           const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
                                       __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
           if (((m + 0x00800080u) & 0x80008000u) != 0) {
-            // infinities: the error-free products would make NaN of them
-            const F2 n0 = f2_mul(y01, sc[0].nsh), n1 = f2_mul(y23, sc[1].nsh);
-            ox01 = f2_fma(x01, sc[0].ch, n0), ox23 = f2_fma(x23, sc[1].ch, n1);
-            oy01 = f2_fma(y01, sc[0].ch, f2_mul(x01, sc[0].sh)), oy23 = f2_fma(y23, sc[1].ch, f2_mul(x23, sc[1].sh));
+            turn2_infinite(x01, y01, sc[0], ox01, oy01);
+            turn2_infinite(x23, y23, sc[1], ox23, oy23);
           } else {
             turn2(x01, y01, sc[0], ox01, oy01);
             turn2(x23, y23, sc[1], ox23, oy23);
