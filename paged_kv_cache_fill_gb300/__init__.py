@@ -493,6 +493,8 @@ def paged_decode_attn_fp8_block_prefix(q, k_cache_fp8, v_cache_fp8, k_scales, v_
 def kv_rope_frequencies(rotary_dim, theta, scaling=KV_ROPE_PLAIN, factor=1.0, trained_len=0.0, low=0.0,
                         high=0.0) -> list[float]:
     """The rotary_dim / 2 frequencies of a rotation, radians per position."""
+    if not 0 <= rotary_dim < 1 << 31:  # (a C uint32 would take it modulo 2^32, past the array)
+        _check("kv_rope_frequencies", KV_ERR_INVALID_ARG)
     freqs = (ctypes.c_double * max(1, rotary_dim // 2))()
     _check("kv_rope_frequencies", lib().kv_rope_frequencies(
         freqs, rotary_dim, theta, scaling, factor, trained_len, low, high))
