@@ -992,9 +992,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 6 : 2) combi
   if (item >= uint64_t(p.num_seqs) * p.num_q_heads) return;
   const uint32_t s = uint32_t(item / p.num_q_heads), h = uint32_t(item % p.num_q_heads);
   const bool plan = plan_fits(p.plan.head, p);
-  // PlanSeq (a plan that was made for fewer sequences holds none for the last ones)
-  const int4 q = plan ? __ldcg(reinterpret_cast<const int4*>(p.plan.seqs + s)) : make_int4(0, 0, 0, 0);
-  const int32_t eff = q.x;
+  // PlanSeq (a plan that was made for fewer sequences holds none for the last ones: its header, for nothing)
+  const int4 q = __ldcg(plan ? reinterpret_cast<const int4*>(p.plan.seqs + s) : reinterpret_cast<const int4*>(p.plan.head));
+  const int32_t eff = plan ? q.x : 0;
   const SeqSpan span = seq_span(__ldg(p.seq_lens + s), eff, p);
   const uint32_t nshared = eff > 0 ? uint32_t(q.y) : 0;
   wait_for_prerequisite();
