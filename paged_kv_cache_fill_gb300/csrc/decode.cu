@@ -133,10 +133,9 @@ struct DecodeParams {
   float score_scale;    // inv_sqrt_d * log2(e)   (times k_scale for FP8)
   float out_scale;      // FP8 V: v_scale / 2^8 (P enters the MMA scaled by 2^8)
   float partial_scale;  // kBlkPartial with block scales, else 1
-  bool bf16_out;        // kFine: the output rows are BF16
-  PrefixView plan;      // with a plan (kFine): each sequence's positions past the ones that its group attends together
-  uint32_t num_groups, plan_sinks;
   uint32_t stages, stage_bytes, k_bytes, v_bytes;  // shared-memory ring geometry
+  PrefixView plan;      // kPrefix, with a plan: each sequence's positions past the ones that its group attends together
+  uint32_t num_groups, plan_sinks;
 };
 
 // -------------------------------------------------------------- item walk
@@ -144,13 +143,14 @@ struct DecodeParams {
 // first ns of them the sink tiles 0.., the others t0... (A tile that holds
 // both sinks and window positions is t0.)
 //
-// With a plan everything counts from `eff`, the end of the positions that the
+// With a plan (kPrefix) everything counts from `eff`, the end of the positions that the
 // sequence's group attends together: length, window and sinks as seen from there.
 struct SeqSpan {
   int32_t len, start, t0, ns, ntiles, eff, sinks;
   __device__ __forceinline__ int32_t tile(int32_t i) const { return i < ns ? i : i - ns + t0; }
 };
 
+template <bool kPrefix>
 __device__ __forceinline__ SeqSpan seq_span(int32_t raw_len, int32_t eff, const DecodeParams& p) {
   SeqSpan s;
   int32_t L = raw_len < 0 ? 0 : raw_len;
@@ -159,9 +159,13 @@ __device__ __forceinline__ SeqSpan seq_span(int32_t raw_len, int32_t eff, const 
     L = int32_t(cap);
     atomicOr(&g_decode_error, kErrSeqLenClamped);
   }
-  s.eff = eff;
-  s.sinks = p.num_sinks > eff ? p.num_sinks - eff : 0;
-  L = L > eff ? L - eff : 0;
+  s.eff = 0;
+  s.sinks = p.num_sinks;
+  if constexpr (kPrefix) {
+    s.eff = eff;
+    s.sinks = p.num_sinks > eff ? p.num_sinks - eff : 0;
+    L = L > eff ? L - eff : 0;
+  }
   s.len = L;
   s.start = (p.sliding_window > 0 && int64_t(L) > int64_t(p.sliding_window))
                 ? int32_t(int64_t(L) - int64_t(p.sliding_window))
@@ -181,20 +185,23 @@ __device__ __forceinline__ int32_t prefix_of(bool plan, uint32_t s, const Decode
 // The producer walks the tile stream 32 sequences at a time: each lane
 // holds one sequence's tile count (times the head groups) and the warp keeps
 // an inclusive prefix of the chunk.
+template <bool kPrefix>
 struct Walker {
   uint32_t chunk_seq;    // first sequence of the cached chunk
   uint64_t chunk_base;   // stream tiles before the chunk
   uint64_t incl;         // inclusive prefix of stream tiles within the chunk (this lane)
   uint64_t chunk_total;  // stream tiles of the chunk
   int32_t raw_len;       // seq_lens of sequence chunk_seq + lane
-  int32_t eff;           // and its prefix
+  int32_t eff;           // and its prefix (with a plan)
 
   __device__ void load(uint32_t first_seq, const DecodeParams& p, uint32_t lane, bool plan) {
     chunk_seq = first_seq;
     const uint32_t s = first_seq + lane;
     raw_len = s < p.num_seqs ? __ldg(p.seq_lens + s) : 0;
-    eff = s < p.num_seqs ? prefix_of(plan, s, p) : 0;
-    incl = s < p.num_seqs ? uint64_t(seq_span(raw_len, eff, p).ntiles) * p.num_head_groups : 0;
+    eff = 0;
+    if constexpr (kPrefix)
+      if (s < p.num_seqs) eff = prefix_of(plan, s, p);
+    incl = s < p.num_seqs ? uint64_t(seq_span<kPrefix>(raw_len, eff, p).ntiles) * p.num_head_groups : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -346,7 +353,10 @@ constexpr bool two_ctas_per_sm() { return kFp8V && D <= 128 && NT == 1; }
 
 constexpr uint32_t kMaxItemHeads = 8;  // heads per item, at most (geometry)
 
-template <bool kFp8, bool kFp8V, bool kBlk, bool kFine, int D, int NT>
+// kPrefix: the call over shared prefixes, with a plan or (short tables) without one, whose rows
+// are BF16. Instances of their own: as a choice made on the device it cost the other
+// calls up to 3.7% (FP8 K, 12 query heads per KV head, 32 sequences of 8,192 positions: 164 -> 170 us).
+template <bool kFp8, bool kFp8V, bool kBlk, bool kFine, bool kPrefix, int D, int NT>
 __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const DecodeParams p) {
@@ -358,6 +368,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   static_assert(kFp8 || !kFp8V, "an FP8 V cache comes with an FP8 K cache");
   static_assert(kFp8V || !kBlk, "block scales come with an FP8 K and V cache");
   static_assert(kFine || !kBlk, "the call with block scales takes sinks too");
+  static_assert(kFine || !kPrefix, "the call over shared prefixes takes sinks too");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   const uint32_t num_consumers = p.heads_per_item * NT;
   const uint64_t wait_ns = pipeline_wait_limit();  // fixed in the product build
   bool plan = false;
-  if constexpr (kFine) {
+  if constexpr (kPrefix) {
     if (p.plan.head) {
       launch_dependents();  // the merge of the partial results
       plan = plan_fits(p.plan.head, p);
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
   if (p.max_splits > 0) {
     uint64_t local = 0;
     for (uint32_t s = threadIdx.x; s < p.num_seqs; s += blockDim.x)
-      local += uint64_t(seq_span(__ldg(p.seq_lens + s), prefix_of(plan, s, p), p).ntiles);
+      local += uint64_t(seq_span<kPrefix>(__ldg(p.seq_lens + s), prefix_of(plan, s, p), p).ntiles);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) local += __shfl_xor_sync(0xffffffffu, local, o);
     if (lane == 0 && local) atomicAdd(reinterpret_cast<unsigned long long*>(&s_total), local);
@@ -434,7 +445,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           if (ok) {
             issued &= ~(1u << stage);  // the stage's previous fill was taken, so it landed
             meta[stage] = StageMeta{int32_t(s), int32_t(hg), int32_t(split), 0, 0, 0,
-                                    kFirst | kLast | kEmpty | base_flags, span.sinks};
+                                    kFirst | kLast | kEmpty | base_flags, kPrefix ? span.sinks : 0};
             mbar_arrive(&full[stage]);
           }
         }
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         if (++stage == p.stages) { stage = 0; phase ^= 1; }
         return;
       }
-      const int32_t skip = span.eff >> p.block_shift;  // (eff is a whole number of blocks)
+      const int32_t skip = kPrefix ? span.eff >> p.block_shift : 0;  // (eff is a whole number of blocks)
       const int32_t* table = p.block_tables + uint64_t(s) * p.max_blocks_per_seq + skip;
       const int32_t tiles_per_block_shift = int32_t(p.block_shift) - 4;  // block_size >= 16
       int32_t cached_first_block = -1;  // first logical block held by the lanes
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
             if (i == tile_begin) flags |= kFirst;
             if (i == tile_end - 1) flags |= kLast;
             meta[stage] = StageMeta{int32_t(s), int32_t(hg), int32_t(split), tile, span.start,
-                                    span.len, flags, span.sinks};
+                                    span.len, flags, kPrefix ? span.sinks : 0};
             // one box per tensor covers all heads of the piece (chunks past
             // the last head are zero-filled and still counted in the box bytes)
             const uint32_t bytes = p.k_bytes + p.v_bytes + ((flags & kFirst) ? q_bytes : 0u);
@@ -517,7 +528,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       // chunk b. The piece of (sequence, head group) range [a, b) that lies in
       // chunk k is its piece k - floor(a / C).
       const uint64_t C = s_chunk, total = s_total;
-      Walker wk;
+      Walker<kPrefix> wk;
       wk.chunk_base = 0;
       wk.load(0, p, lane, plan);
       uint64_t g = blockIdx.x * C;
@@ -533,8 +544,9 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         const uint64_t rel = g - wk.chunk_base;
         const uint32_t sl = __ffs(__ballot_sync(0xffffffffu, wk.incl > rel)) - 1;
         const uint32_t s = wk.chunk_seq + sl;
-        const SeqSpan span =
-            seq_span(__shfl_sync(0xffffffffu, wk.raw_len, sl), __shfl_sync(0xffffffffu, wk.eff, sl), p);
+        int32_t eff = 0;
+        if constexpr (kPrefix) eff = __shfl_sync(0xffffffffu, wk.eff, sl);
+        const SeqSpan span = seq_span<kPrefix>(__shfl_sync(0xffffffffu, wk.raw_len, sl), eff, p);
         const uint64_t nt = uint64_t(span.ntiles);  // > 0: the ballot skips empty sequences
         const uint64_t seq_base = wk.chunk_base + __shfl_sync(0xffffffffu, wk.incl, sl) - nt * p.num_head_groups;
         const uint32_t hg = uint32_t((g - seq_base) / nt);
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         if (e == b && lane == 0) p.ws_count[uint64_t(s) * p.num_head_groups + hg] = split + 1;
         if (ok)
           emit(s, hg, split, span, int32_t(g - a), int32_t(e - a),
-               (g == a && e == b && span.eff == 0) ? kSingle : 0);
+               (g == a && e == b && (!kPrefix || span.eff == 0)) ? kSingle : 0);
         g = e;
       }
     } else {
@@ -553,7 +565,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       const uint64_t items = uint64_t(p.num_seqs) * p.num_head_groups;
       for (uint64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
         const uint32_t s = uint32_t(it / p.num_head_groups), hg = uint32_t(it % p.num_head_groups);
-        const SeqSpan span = seq_span(__ldg(p.seq_lens + s), 0, p);
+        const SeqSpan span = seq_span<false>(__ldg(p.seq_lens + s), 0, p);
         emit(s, hg, 0, span, 0, span.ntiles, kSingle);
       }
     }
@@ -585,7 +597,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
           if (!mbar_wait(&full[st], (issued_parity >> st) & 1u)) atomicOr(&g_decode_error, kErrWaitTimeout);
     }
     // this grid is done no sooner than the shared positions' before it, for the merge that waits for this one
-    if constexpr (kFine)
+    if constexpr (kPrefix)
       if (p.plan.head) wait_for_prerequisite();
     return;
   }
@@ -731,7 +743,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       s[3] *= hs1;
       // ---- mask positions outside [start, len) and the sinks
       const int32_t p0 = mt.tile * kTile;
-      const int32_t sinks = kFine ? mt.sinks : 0;
+      const int32_t sinks = kPrefix ? mt.sinks : kFine ? p.num_sinks : 0;
       const bool boundary = (p0 < mt.start && p0 + kTile > sinks) || p0 + kTile > mt.len;
       auto attended = [&](int32_t pos) { return (pos >= mt.start || pos < sinks) && pos < mt.len; };
       if (boundary) {
@@ -851,7 +863,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
       if (mt.flags & kSingle) {
         const float inv0 = (mt.flags & kEmpty) ? 0.0f : sc0 / l0;
         const float inv1 = (mt.flags & kEmpty) ? 0.0f : sc1 / l1;
-        if (kFine && p.bf16_out) {
+        if constexpr (kPrefix) {
           // (the rows' halves of 32-bit words are written apart: a lane holds rows g8
           // and g8 + 8 of V^T, or with an E4M3 V adjacent dims)
           uint16_t* b0 = reinterpret_cast<uint16_t*>(p.output) + (uint64_t(mt.seq) * p.num_q_heads + hq0) * D;
@@ -869,7 +881,7 @@ __global__ void __launch_bounds__(32 * 9, two_ctas_per_sm<kFp8V, D, NT>() ? 2 : 
         float* o0 = p.output + (uint64_t(mt.seq) * p.num_q_heads + hq0) * D;
         float* o1 = o0 + D;
 #pragma unroll
-        for (int i = 0; i < D / 16 && !(kFine && p.bf16_out); ++i) {
+        for (int i = 0; i < (kPrefix ? 0 : D / 16); ++i) {
           if constexpr (kFp8V) {
             // accumulator rows g8 / g8+8 are dims 2g8 / 2g8+1
             const uint32_t d = i * 16 + 2 * g8;
@@ -941,7 +953,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Decod
   if (item >= uint64_t(p.num_seqs) * p.num_q_heads) return;
   const uint32_t s = uint32_t(item / p.num_q_heads), h = uint32_t(item % p.num_q_heads);
   float* out = p.output + item * D;
-  const SeqSpan span = seq_span(__ldg(p.seq_lens + s), 0, p);
+  const SeqSpan span = seq_span<false>(__ldg(p.seq_lens + s), 0, p);
   if (span.ntiles == 0) {
 #pragma unroll
     for (uint32_t k = 0; k < D / 32; ++k) out[lane + 32 * k] = 0.0f;
@@ -995,7 +1007,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, kBatch == 2 ? 6 : 2) combi
   // PlanSeq (a plan that was made for fewer sequences holds none for the last ones: its header, for nothing)
   const int4 q = __ldcg(plan ? reinterpret_cast<const int4*>(p.plan.seqs + s) : reinterpret_cast<const int4*>(p.plan.head));
   const int32_t eff = plan ? q.x : 0;
-  const SeqSpan span = seq_span(__ldg(p.seq_lens + s), eff, p);
+  const SeqSpan span = seq_span<true>(__ldg(p.seq_lens + s), eff, p);
   const uint32_t nshared = eff > 0 ? uint32_t(q.y) : 0;
   wait_for_prerequisite();
   uint32_t nown = 0;
@@ -1163,13 +1175,13 @@ Geometry geometry(bool fp8, bool fp8_v, uint32_t head_dim, uint32_t num_kv_heads
   return g;
 }
 
-template <bool kFp8, bool kFp8V, bool kBlk, bool kFine, int D, int NT>
+template <bool kFp8, bool kFp8V, bool kBlk, bool kFine, int D, int NT, bool kPrefix = false>
 int launch_decode_t(const DecodeArgs& a, cudaStream_t stream, const Geometry& geo, DecodeParams& p) {
   CUtensorMap mk, mv;
   if (!encode_pool_map(&mk, a.k_cache, kFp8, a.num_kv_heads, D, geo.heads_per_item) ||
       !encode_pool_map(&mv, a.v_cache, kFp8V, a.num_kv_heads, D, geo.heads_per_item))
     return KV_ERR_CUDA;
-  auto kern = decode_kernel<kFp8, kFp8V, kBlk, kFine, D, NT>;
+  auto kern = decode_kernel<kFp8, kFp8V, kBlk, kFine, kPrefix, D, NT>;
   // The dynamic shared-memory opt-in is set once per device and size (so
   // that calls made while a stream is being captured into a CUDA graph after
   // a first eager call issue no attribute change).
@@ -1185,7 +1197,7 @@ int launch_decode_t(const DecodeArgs& a, cudaStream_t stream, const Geometry& ge
   const DeviceInfo& dev = device_info();
   const uint32_t threads = 32 * (1 + geo.heads_per_item * geo.nt);
   if (geo.ctas_per_sm > 1 && !two_ctas_per_sm<kFp8V, D, NT>()) return KV_ERR_CUDA;  // not reached
-  if constexpr (kFine && D <= 128) {
+  if constexpr (kPrefix) {
     if (p.plan.head) {
       // beside the grid before it, from where that one's CTAs have left an SM; the merge beside this one
       cudaLaunchAttribute attr{};
@@ -1288,7 +1300,6 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.score_scale = a.inv_sqrt_d * kLog2e * (a.fp8 ? a.k_scale : 1.0f);
   p.out_scale = fp8_v ? a.v_scale * (1.0f / 256.0f) : 1.0f;
   p.partial_scale = a.k_scales ? kBlkPartial : 1.0f;
-  p.bf16_out = a.bf16_out;
   p.plan = a.plan;
   p.num_groups = a.plan_groups;
   p.plan_sinks = a.num_sinks;
@@ -1323,7 +1334,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     }
   }
 
-  const int key = (a.fine ? 1000 : 0) + (a.k_scales ? 300 : fp8_v ? 200 : a.fp8 ? 100 : 0) +
+  const int key = (a.bf16_out ? 2000 : a.fine ? 1000 : 0) + (a.k_scales ? 300 : fp8_v ? 200 : a.fp8 ? 100 : 0) +
                   int(a.head_dim / 64) * 10 + int(geo.nt);
   switch (key) {
     case 11: return launch_decode_t<false, false, false, false, 64, 1>(a, stream, geo, p);
@@ -1368,6 +1379,22 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     case 1322: return launch_decode_t<true, true, true, true, 128, 2>(a, stream, geo, p);
     case 1341: return launch_decode_t<true, true, true, true, 256, 1>(a, stream, geo, p);
     case 1342: return launch_decode_t<true, true, true, true, 256, 2>(a, stream, geo, p);
+    case 2011: return launch_decode_t<false, false, false, true, 64, 1, true>(a, stream, geo, p);
+    case 2012: return launch_decode_t<false, false, false, true, 64, 2, true>(a, stream, geo, p);
+    case 2021: return launch_decode_t<false, false, false, true, 128, 1, true>(a, stream, geo, p);
+    case 2022: return launch_decode_t<false, false, false, true, 128, 2, true>(a, stream, geo, p);
+    case 2111: return launch_decode_t<true, false, false, true, 64, 1, true>(a, stream, geo, p);
+    case 2112: return launch_decode_t<true, false, false, true, 64, 2, true>(a, stream, geo, p);
+    case 2121: return launch_decode_t<true, false, false, true, 128, 1, true>(a, stream, geo, p);
+    case 2122: return launch_decode_t<true, false, false, true, 128, 2, true>(a, stream, geo, p);
+    case 2211: return launch_decode_t<true, true, false, true, 64, 1, true>(a, stream, geo, p);
+    case 2212: return launch_decode_t<true, true, false, true, 64, 2, true>(a, stream, geo, p);
+    case 2221: return launch_decode_t<true, true, false, true, 128, 1, true>(a, stream, geo, p);
+    case 2222: return launch_decode_t<true, true, false, true, 128, 2, true>(a, stream, geo, p);
+    case 2311: return launch_decode_t<true, true, true, true, 64, 1, true>(a, stream, geo, p);
+    case 2312: return launch_decode_t<true, true, true, true, 64, 2, true>(a, stream, geo, p);
+    case 2321: return launch_decode_t<true, true, true, true, 128, 1, true>(a, stream, geo, p);
+    case 2322: return launch_decode_t<true, true, true, true, 128, 2, true>(a, stream, geo, p);
     default: return KV_ERR_UNSUPPORTED;
   }
 }

@@ -168,7 +168,7 @@ struct DecodeArgs {
   void* workspace;
   size_t workspace_bytes;
   bool fine;  // shorter sums and finer weights (decode.cu)
-  bool bf16_out;           // the output rows are BF16 (with `fine`)
+  bool bf16_out;           // the call over shared prefixes (with `fine`), whose output rows are BF16
   PrefixView plan;         // with a plan: positions past the shared ones, merged with its pieces' partial results
   uint32_t plan_groups;
 };
