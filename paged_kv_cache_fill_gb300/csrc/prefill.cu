@@ -461,6 +461,11 @@ __global__ void __launch_bounds__(32 * 12, 1)
   // (kPrefix: all, so that the loads of the next tile never wait for a conversion)
   constexpr uint32_t kSoftKeys = !kFp8V || Lay::kV8Ring ? 0 : kBlk || kPrefix ? kTcBN : kTcBN / 2;
   constexpr bool kSelfConverts = kFp8V && kSoftKeys < kTcBN;
+  // V tile j converted at the start of step j instead of at the end of step j - 1, off the path of
+  // that step's PV product either way (us at the end / at the start, 8 x 1,024 queries over
+  // 4,096 to 8,192 positions, head_dim 128: BF16 591 / 595, FP8 K 604 / 589, FP8 K and V 562 / 571,
+  // block scales 610 / 605)
+  constexpr bool kLateV = kPrefix || (kFp8 && (!kFp8V || kBlk));
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -1218,13 +1223,12 @@ __global__ void __launch_bounds__(32 * 12, 1)
       };
       float m_run = -INFINITY, l_run = 0.0f;
       [[maybe_unused]] float far_m = -INFINITY, far_l = 0.0f;  // kBlk: largest score and sum of the groups far below
-      bool ok = true;
+      bool ok = kLateV || T == 0 || convert_v(0);
       // n: this Q tile's steps, over key tiles j
       for (int32_t j = split ? int32_t(t) : 0, n = 0; j < T && ok; j += split ? 2 : 1, ++n) {
-        // V tile j, off the path of the PV product before it. raw_v: into the stage that this
-        // Q tile's last PV product has freed
+        // raw_v: into the stage that this Q tile's last PV product has freed
         if (raw_v) ok = n == 0 || __all_sync(0xffffffffu, mbar_wait(&o_full[t], uint32_t(n - 1) & 1));
-        if (!split || raw_v) ok = ok && convert_v(j);
+        if (kLateV && (!split || raw_v)) ok = ok && convert_v(j);
         if (!ok) break;
         // kBlk: the groups' scales (the row's included), while S is on its way
         [[maybe_unused]] float ka[kGroups], vl[kGroups];
@@ -1414,6 +1418,8 @@ __global__ void __launch_bounds__(32 * 12, 1)
         // had run its product
         if constexpr (kPrefix && !kFp8V)
           if (split) ok = convert_v(j);
+        if constexpr (!kLateV)
+          if (j + 1 < T) ok = convert_v(j + 1);
       }
       if (!ok && lane == 0) atomicOr(&g_prefill_error, kErrWaitTimeout);
       // ---- O / l to the output row
