@@ -230,7 +230,9 @@ PAGEDKV_API int kv_rope_table(uint32_t *table, const double *freqs, uint32_t rot
 /* Rotates num_heads heads of each row of x (bf16, row t at element t * x_stride)
  * into out (row t at t * out_stride); the angles are exact for any int32 position
  * and each result is within 1 BF16 ulp of the exactly rounded one, or within 2^-38 of
- * |x| + |y| where the two products cancel beyond that. `inverse`
+ * |a| (|x| + |y|) where the two products cancel beyond that (for x and y below 2^127;
+ * larger ones may overflow on the way). A pair that holds an infinity or a NaN gives what
+ * the formula gives, and no other pair is touched by it. `inverse`
  * nonzero turns back by the same angles (with the same amplitude): the gradient of
  * the rotation, or (with positions that are differences) rows moved to others.
  *   out        may be x itself, with the same stride; no other overlap.
@@ -246,7 +248,8 @@ PAGEDKV_API int kv_rope(const kv_bf16_t *x, kv_bf16_t *out, const uint32_t *rope
  * rotated into row `slot` of the K pool, and its values copied into the V pool
  * (bf16), or keys and values stored as E4M3(x / scale), as kv_write_fp8k and
  * kv_write_fp8 do, the rotated key in 32 bits (its code is the correctly rounded one
- * except within ~2^-21, relative, of the midpoint between two). A negative slot:
+ * except where the rotated key is within 2^-21 of itself, or within 2^-38 of its pair's
+ * |a| (|x| + |y|), of a midpoint between two codes). A negative slot:
  * nothing is written for the token, its row of q_out included.
  *   q, key, value  device bf16 rows at element strides, such as parts of a fused
  *                  projection's rows; any alignment and strides.
@@ -510,7 +513,11 @@ PAGEDKV_API int paged_prefill_attn_fp8_sinks(const kv_bf16_t *q, const kv_e4m3_t
  * that is longer than the block and attends it has the same table entry; groups that
  * share nothing, or too little to be worth it, are attended member by member. So the
  * groups are a hint: the result is that of the `_sinks` call (the block-scaled one)
- * over the same tables, lengths and window, in BF16, whatever they are.
+ * over the same tables, lengths and window, in BF16, whatever they are - but for the
+ * roundings and for values that are not finite, both below.
+ * What is worth it is decided for BF16 caches (a plan knows no type): over 8-bit caches
+ * pairs, and groups of four and eight over few positions, are slower shared than alone;
+ * leave such groups out of group_start.
  *   plan         device memory of kv_prefix_plan_bytes(...), 16-byte aligned, written.
  *   group_start  device int32[num_groups + 1], non-decreasing, in [0, num_seqs] (otherwise
  *                bit 2 of the fault word is set and nothing is shared).
@@ -523,7 +530,8 @@ PAGEDKV_API int paged_prefill_attn_fp8_sinks(const kv_bf16_t *q, const kv_e4m3_t
  * arguments (shapes, num_groups, window, sinks) sets bit 6 of the fault word and is not
  * used: each sequence is attended by itself.
  * Supported: head_dim 64 or 128, block_size a power of two in [16, 256], num_groups up
- * to 4,096. Tables of at most 128 positions need no plan (none is written).
+ * to 4,096. Tables of at most 128 positions need no plan: none is written, and the
+ * attention calls do not look at the buffer (which they take all the same).
  * ---------------------------------------------------------------------- */
 PAGEDKV_API size_t kv_prefix_plan_bytes(uint32_t num_seqs, uint32_t num_groups, uint32_t num_q_heads,
                                         uint32_t num_kv_heads);
@@ -537,9 +545,12 @@ PAGEDKV_API int kv_prefix_plan(void *plan, const int32_t *block_tables, const in
  * inv_sqrt_d > 0, the plan after the lengths and num_groups after num_seqs. The rows
  * are BF16, bf16[num_seqs, num_q_heads, head_dim], 8-byte aligned: the shared
  * positions' softmax weights enter the products rounded to 11 bits, as the prefill's.
- * BF16 V values are held as the prefill holds them (magnitudes below 2^24), and a V
- * value that is not finite makes the rows of every member of its group non-finite, and
- * the other way round a sequence's own such value its own row alone.
+ * The shared positions' BF16 V values are held as f16 of v 2^-8: exactly for 2^-9 <= |v| <
+ * 2^24, within 2^-17 below, where the `_sinks` calls hold any value exactly (values of
+ * order 10^-3 are off by up to 0.8%); own positions and E4M3 values exactly. A shared V
+ * value that is not finite, or a BF16 one of 2^24 or more, makes the rows that attend it
+ * non-finite, and may make those of any member of its group so (a weight of zero times
+ * it is a NaN); one among a sequence's own positions makes that sequence's rows alone.
  * A workspace of at least kv_prefix_workspace_bytes(...) has to be registered by
  * kv_set_decode_workspace, else KV_ERR_UNSUPPORTED (tables of at most 128 positions
  * need none and are attended without the plan).

@@ -451,7 +451,8 @@ def paged_decode_attn_bf16_prefix(q, k_cache, v_cache, output, block_tables, seq
                                   num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d,
                                   q_stride, sliding_window, num_sinks, stream=None):
     """Paged decode (with sinks) that reads what groups of sequences share once for each
-    group; `output` is BF16. Wants a workspace of kv_prefix_workspace_bytes."""
+    group; `output` is BF16. Wants a workspace of kv_prefix_workspace_bytes. Small BF16
+    values of shared positions are held to 2^-17 (the header says where)."""
     _check("paged_decode_attn_bf16_prefix", lib().paged_decode_attn_bf16_prefix(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(output), _ptr(block_tables), _ptr(seq_lens), _ptr(plan),
         max_blocks_per_seq, num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, inv_sqrt_d,
@@ -513,7 +514,8 @@ def kv_rope_table(freqs, amplitude=1.0) -> torch.Tensor:
 
 def kv_rope(x, out, rope_table, positions, num_tokens, num_heads, head_dim, rotary_dim, x_stride, out_stride,
             interleaved=False, inverse=False, stream=None):
-    """Rotate the heads of BF16 rows by their positions (or back, `inverse`: the gradient)."""
+    """Rotate the heads of BF16 rows by their positions (or back, `inverse`: the gradient).
+    x is rows at x_stride from the tensor's start on (part of wider rows: x.view(-1)[a:])."""
     _check("kv_rope", lib().kv_rope(
         _ptr(x), _ptr(out), _ptr(rope_table), _ptr(positions), num_tokens, num_heads, head_dim, rotary_dim, x_stride,
         out_stride, interleaved, inverse, _stream(stream)))
@@ -522,7 +524,12 @@ def kv_rope(x, out, rope_table, positions, num_tokens, num_heads, head_dim, rota
 def kv_append_rope_bf16(q, key, value, q_out, k_cache, v_cache, rope_table, positions, slot_mapping, num_tokens,
                         num_q_heads, num_kv_heads, head_dim, rotary_dim, block_size, q_stride, key_stride,
                         value_stride, q_out_stride, interleaved=False, stream=None):
-    """Rotate a step's queries into q_out and its keys into the cache, and write its values."""
+    """Rotate a step's queries into q_out and its keys into the cache, and write its values.
+
+    q, key and value are rows at the strides given, and a tensor only says where the first
+    one begins: of a fused projection qkv [num_tokens, row] pass flat = qkv.view(-1),
+    flat[q_width:] and flat[q_width + k_width:] with `row` for each stride (qkv[:, a:b]
+    is not contiguous and is refused)."""
     _check("kv_append_rope_bf16", lib().kv_append_rope_bf16(
         _ptr(q), _ptr(key), _ptr(value), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(rope_table),
         _ptr(positions), _ptr(slot_mapping), num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim, block_size,

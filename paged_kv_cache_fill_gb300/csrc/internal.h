@@ -144,6 +144,9 @@ struct PlanArgs {
 // (13 MB) 38 / 36 and 44 / 40, over 4,096 (52 MB) 40 / 47 and 45 / 51; 8 groups of 4 over 512 (20 MB) 37 / 39 and
 // 42 / 40, over 2,048 (80 MB) 49 / 62 and 53 / 55; 64 members over 512 (62 MB) 37 / 44 and 46 / 44, over 2,048 (250 MB)
 // 40 / 80 and 45 / 70; 32 pairs over 1,024 (32 MB) 72 / 80 and 78 / 59, over 4,096 (128 MB) 147 / 202 and 149 / 125.
+// So the limit serves BF16 and large groups. Over 8-bit caches it lets small groups through that are slower shared
+// (the last figure, and 16 groups of 4 over 512: 46 / 25), which callers leave out of group_start: a plan that is to
+// decide that would have to know the type.
 constexpr uint64_t kMinSavedBytes = 40ull << 20;
 int launch_prefix_plan(const PlanArgs& a, cudaStream_t stream);
 cudaError_t read_and_clear_prefix_error(uint32_t* bits);

@@ -29,6 +29,7 @@ constexpr uint32_t kMinPieceTiles = 2;
 //   256   90, -     78, 89     63, 72
 //   512   128, 138  124, 100   88, 76
 //   1024  202, 175  202, 119   148, 85
+// (8-bit caches, whose decode reads half as much: internal.h, kMinSavedBytes)
 constexpr uint32_t kMinGroupKeys = 1024;
 
 struct PlanHeader {

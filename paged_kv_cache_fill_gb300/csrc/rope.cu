@@ -9,14 +9,14 @@
 // (kv_rope_table) holds f_i as a 96-bit fraction of a turn and a_i, so P f_i is
 // reduced exactly for any int32 position, and sines and cosines come to 2^-43
 // (rope.cuh). The rotation (turn2) is within 2^-22 of each result and 2^-38 of
-// its pair's magnitude, and is rounded once: to BF16, or, divided by the cache's
+// its pair's magnitude (times the amplitude), and is rounded once: to BF16, or, divided by the cache's
 // scale, to E4M3.
 //
 // Every row is read once and written once, so HBM bounds the long calls and the
 // instructions (122 per warp and 16 bytes a lane) come close behind: 120,000
 // tokens of 32 + 2 x 8 heads of 128 into an E4M3 K and a BF16 V take 440 us, 6.4
 // TB/s or 95% of the copy rate; 9,001 tokens of 15 + 2 x 3 heads of 256 into E4M3
-// caches 42 us (63%); 8,192 rows of 32 heads of 128, 134 MB, 27.2 us (73%); one
+// caches 43 us (62%); 8,192 rows of 32 heads of 128, 134 MB, 27.2 us (73%); one
 // token 4.2 us, the launch. With the rotation of rope.cuh, which has nearly twice
 // the operations, they were 480, 44 and 29.4 us. A warp handles 256 /
 // head_dim tokens at a time with head_dim / 8 lanes per token; a lane owns the
